@@ -32,7 +32,9 @@ __all__ = [
     "hkv_evict_select", "hkv_write_slots", "hkv_lse_merge", "hkv_decode_step", "hkv_decode_step_heads",
     "hkv_decode_step_ragged", "hkv_split_select", "hkv_lse_merge_n", "hkv_retrieve_topk_paged",
     "hkv_sparse_attend_paged", "hkv_decode_step_paged", "hkv_normw_workspace_bytes", "normw_workspace",
-    "hkv_decode_step_normw", "normw_decode_workspace", "hkv_debug_set", "EXPORTS",
+    "hkv_decode_step_normw", "normw_decode_workspace", "hkv_debug_set", "RopeParams", "hkv_append_paged",
+    "hkv_append_paged_workspace_bytes", "append_workspace", "hkv_prefill_attend_paged", "hkv_prefill_workspace_bytes",
+    "prefill_workspace", "hkv_shared_attend_paged", "hkv_shared_workspace_bytes", "shared_workspace", "EXPORTS",
 ]
 
 HKV_OK, HKV_ERR_INVALID_ARG, HKV_ERR_UNSUPPORTED, HKV_ERR_CAPACITY = 0, -1, -2, -3
@@ -48,7 +50,8 @@ EXPORTS = (
     "hkv_evict_select", "hkv_write_slots", "hkv_lse_merge", "hkv_decode_step", "hkv_decode_step_heads",
     "hkv_decode_step_ragged", "hkv_split_select", "hkv_lse_merge_n", "hkv_retrieve_topk_paged",
     "hkv_sparse_attend_paged", "hkv_decode_step_paged", "hkv_normw_workspace_bytes", "hkv_decode_step_normw",
-    "hkv_debug_set",
+    "hkv_debug_set", "hkv_append_paged", "hkv_append_paged_workspace_bytes", "hkv_prefill_attend_paged",
+    "hkv_prefill_workspace_bytes", "hkv_shared_attend_paged", "hkv_shared_workspace_bytes",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -67,6 +70,20 @@ class hkv_hash(ctypes.Structure):
         ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("R", ctypes.c_void_p), ("W1", ctypes.c_void_p), ("b1", ctypes.c_void_p),
         ("W2", ctypes.c_void_p), ("b2", ctypes.c_void_p), ("packed", ctypes.c_void_p),
+    ]
+
+
+class hkv_rope(ctypes.Structure):
+    _fields_ = [
+        ("pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_uint8 * 64),
+    ]
+
+
+class hkv_score(ctypes.Structure):
+    _fields_ = [
+        ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p), ("q_first", ctypes.c_void_p),
     ]
 
 
@@ -106,6 +123,15 @@ _SIGS = {
                                    _I, _I, _F, _P, _P, _P, _P, _P, _SZ, _P, _P]),
     "hkv_sparse_attend_paged": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I64, _I64, _I, _I64, _P, _I, _I, _I, _F, _P, _P,
                                      _P, _SZ, _P, _P]),
+    "hkv_append_paged": (_I, [ctypes.POINTER(hkv_hash), _I, ctypes.POINTER(hkv_rope), _I, _I64, _I, _I, _P, _I64, _P, _I64,
+                              _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _P, _SZ, _P, _P]),
+    "hkv_append_paged_workspace_bytes": (_SZ, [ctypes.POINTER(hkv_hash), _I64, _I]),
+    "hkv_prefill_attend_paged": (_I, [_I, _I64, _I, _I, _I, _P, _I64, _P, _P, _P, _I64, _I64, _I, _P, _P, _I, _I64, _F,
+                                      ctypes.POINTER(hkv_score), _P, _P, _P, _SZ, _P, _P]),
+    "hkv_prefill_workspace_bytes": (_SZ, [_I, _I64, _I, _I, _I, _I, _I64]),
+    "hkv_shared_attend_paged": (_I, [_I, _I, _I, _I, _P, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _P, _I64, _F,
+                                     ctypes.POINTER(hkv_score), _P, _P, _P, _SZ, _P, _P]),
+    "hkv_shared_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I64, _I64]),
     "hkv_write_slots": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]),
 }
 _lib = None
@@ -655,3 +681,202 @@ def hkv_decode_step_normw(q, k_codes, norms, K, V, n_tokens: int, n_sink: int, n
                                     _ptr(V), cap, n_tokens, n_sink, n_local, top_k, scale, _ptr(q_codes), _ptr(idx),
                                     _ptr(score), _ptr(out), _ptr(lse), _ptr(ws), nbytes, _ptr(status),
                                     _stream(stream)))
+
+
+class RopeParams:
+    """Rotary positions (the C struct hkv_rope).  inv_freq [pairs] fp32 on the device; pair i is the elements
+    (i, i + pairs) of a head, or (2 i, 2 i + 1) when interleaved.  sections: how many pairs each position axis turns,
+    in order (their sum is pairs); axis: instead, the axis of every pair."""
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, sections=None, axis=None):
+        _need(inv_freq, "inv_freq", torch.float32)
+        pairs = inv_freq.numel()
+        if inv_freq.dim() != 1 or pairs > 64 or pairs % 8:
+            raise ValueError("inv_freq must be [pairs], pairs a multiple of 8 up to 64")
+        if axis is None:
+            sections = (pairs,) if sections is None else tuple(int(n) for n in sections)
+            if any(n < 0 for n in sections) or sum(sections) != pairs:
+                raise ValueError(f"sections {sections} do not add up to {pairs} pairs")
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+            n_axes = len(sections)
+        else:
+            axis = [int(a) for a in axis]
+            n_axes = max(axis, default=0) + 1
+        if len(axis) != pairs or min(axis, default=0) < 0 or not 1 <= n_axes <= 4:
+            raise ValueError("axis must name one of at most 4 position axes for every pair")
+        self.inv_freq, self.pairs, self.n_axes = inv_freq, pairs, n_axes
+        self.c = hkv_rope(pairs, int(interleaved), n_axes, 0, inv_freq.data_ptr(), (ctypes.c_uint8 * 64)(*axis))
+
+
+def _here(*tensors) -> None:
+    """Every tensor is on the current device, on whose stream the call is issued."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> None:
+    """[T, heads, 128] with dense heads; the rows may be further apart (e.g. a slice of a fused projection)."""
+    _need(t, name, dtype, shape=shape, contiguous=False)
+    if t.numel() and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name} must have dense heads")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * 128)
+
+
+def hkv_append_paged_workspace_bytes(h: Optional[HashParams], T: int, Hkv: int) -> int:
+    return lib().hkv_append_paged_workspace_bytes(None if h is None else ctypes.byref(h.c), T, Hkv)
+
+
+def append_workspace(h: Optional[HashParams], T: int, Hkv: int, device=None) -> Optional[torch.Tensor]:
+    """The workspace of hkv_append_paged, or None when it needs none (bf16 LSH, SIGN, no hash)."""
+    n = hkv_append_paged_workspace_bytes(h, T, Hkv)
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def hkv_append_paged(h: Optional[HashParams], k_new, v_new, K_pool, V_pool, page_table, cu_new, n_past, codes_pool=None,
+                     norms_pool=None, rope: Optional[RopeParams] = None, positions=None, q=None, q_out=None, ws=None,
+                     status=None, stream=None) -> None:
+    """Appends a ragged batch of new tokens to a paged cache, turning keys (and queries) by their rotary positions.
+    k_new, v_new [T, Hkv, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; page_table
+    [B, max_pages], cu_new [B + 1], n_past [B] int32; codes_pool [num_pages, Hkv, page_size, W] with a hash; positions
+    int32 [n_axes, T] (default: the position in the cache); q, q_out [T, Hq, 128] (q_out may be q)."""
+    num_pages, Hkv, page_size, d = K_pool.shape
+    T, B = k_new.shape[0], page_table.shape[0]
+    _need(k_new, "k_new", (torch.bfloat16, torch.float32), contiguous=False)
+    dt = k_new.dtype
+    _need_rows(k_new, "k_new", dt, (T, Hkv, 128))
+    _need_rows(v_new, "v_new", dt, (T, Hkv, 128))
+    _need(K_pool, "K_pool", dt, shape=(num_pages, Hkv, page_size, 128))
+    _need(V_pool, "V_pool", dt, shape=(num_pages, Hkv, page_size, 128))
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
+    _need(n_past, "n_past", torch.int32, shape=(B,))
+    if h is None and (codes_pool is not None or norms_pool is not None):
+        raise ValueError("codes_pool and norms_pool need a hash")
+    if h is not None:
+        if codes_pool is None:
+            raise ValueError("a hash needs codes_pool")
+        _need(codes_pool, "codes_pool", _U32, shape=(num_pages, Hkv, page_size, h.words))
+    if norms_pool is not None:
+        _need(norms_pool, "norms_pool", (torch.float16, torch.int16), shape=(num_pages, Hkv, page_size))
+    if positions is not None:
+        _need(positions, "positions", torch.int32, shape=(1 if rope is None else rope.n_axes, T))
+    Hq = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        Hq = q.shape[1]
+        _need_rows(q, "q", dt, (T, Hq, 128))
+        _need_rows(q_out, "q_out", dt, (T, Hq, 128))
+    _here(k_new, v_new, K_pool, V_pool, page_table, cu_new, n_past, codes_pool, norms_pool, positions, q, q_out, ws, status,
+          None if rope is None else rope.inv_freq)
+    _ok(lib().hkv_append_paged(
+        None if h is None else ctypes.byref(h.c), _dtype_code(k_new), None if rope is None else ctypes.byref(rope.c), B, T,
+        Hq, Hkv, _ptr(q), 0 if q is None else _row_stride(q), _ptr(q_out), 0 if q is None else _row_stride(q_out),
+        _ptr(k_new), _row_stride(k_new), _ptr(v_new), _row_stride(v_new), _ptr(cu_new), _ptr(n_past), _ptr(positions),
+        _ptr(K_pool), _ptr(V_pool), _ptr(codes_pool), _ptr(norms_pool), _ptr(page_table), page_table.shape[1], num_pages,
+        page_size, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+
+
+def _score(softcap, window, slopes, prefix_len, q_first, B, T, Hq) -> hkv_score:
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, shape=(Hq,))
+    if prefix_len is not None:
+        _need(prefix_len, "prefix_len", torch.int32, shape=(B,))
+    if q_first is not None:
+        _need(q_first, "q_first", torch.int32, shape=(T,))
+    return hkv_score(float(softcap), int(window), *(None if t is None else t.data_ptr()
+                                                    for t in (slopes, prefix_len, q_first)))
+
+
+def hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, dtype: int) -> int:
+    return lib().hkv_prefill_workspace_bytes(B, T, Hq, Hkv, dtype, max_q, n_tokens_max)
+
+
+def _zeroed(n: int, device) -> Optional[torch.Tensor]:
+    return None if n == 0 else torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def prefill_workspace(B, Hq, Hkv, T, max_q, n_tokens_max, dtype=torch.bfloat16, device=None) -> Optional[torch.Tensor]:
+    """A zero-filled workspace for hkv_prefill_attend_paged, or None when this shape needs none."""
+    code = _dtype_code(torch.empty(0, dtype=dtype))
+    return _zeroed(hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, code), device)
+
+
+def hkv_prefill_attend_paged(q, K_pool, V_pool, page_table, cu_q, n_tokens_b, max_q: int, n_tokens_max: int, out, lse=None,
+                             scale: Optional[float] = None, softcap: float = 0.0, window: int = 0, slopes=None,
+                             prefix_len=None, q_first=None, ws=None, status=None, stream=None) -> None:
+    """Causal attention of a ragged batch's new tokens over their paged caches (new tokens included).
+    q [T, Hq, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; page_table [B, max_pages],
+    cu_q [B + 1], n_tokens_b [B] int32; out [T, Hq, 128] in q's dtype; lse [T, Hq] fp32.  softcap, slopes [Hq], window,
+    prefix_len [B] and q_first [T] shape the scores and the mask (hkv_score in the header)."""
+    T, Hq, d = q.shape
+    num_pages, Hkv, page_size, _ = K_pool.shape
+    B = page_table.shape[0]
+    _need(q, "q", (torch.bfloat16, torch.float32), contiguous=False)
+    _need_rows(q, "q", q.dtype, (T, Hq, 128))
+    _need(K_pool, "K_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
+    _need(V_pool, "V_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need(cu_q, "cu_q", torch.int32, shape=(B + 1,))
+    _need(n_tokens_b, "n_tokens_b", torch.int32, shape=(B,))
+    _need(out, "out", q.dtype, shape=(T, Hq, 128))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, shape=(T, Hq))
+    sc = _score(softcap, window, slopes, prefix_len, q_first, B, T, Hq)
+    _here(q, K_pool, V_pool, page_table, cu_q, n_tokens_b, out, lse, slopes, prefix_len, q_first, ws, status)
+    _ok(lib().hkv_prefill_attend_paged(
+        B, T, Hq, Hkv, _dtype_code(q), _ptr(q), _row_stride(q), _ptr(K_pool), _ptr(V_pool), _ptr(page_table),
+        page_table.shape[1], num_pages, page_size, _ptr(cu_q), _ptr(n_tokens_b), max_q, n_tokens_max,
+        1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+
+
+def hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, dtype: int) -> int:
+    return lib().hkv_shared_workspace_bytes(B, Hq, Hkv, dtype, n_prefix, n_own_max)
+
+
+def shared_workspace(B, Hq, Hkv, n_prefix, n_own_max, dtype=torch.bfloat16, device=None) -> Optional[torch.Tensor]:
+    """A zero-filled workspace for hkv_shared_attend_paged, or None when this shape needs none."""
+    code = _dtype_code(torch.empty(0, dtype=dtype))
+    return _zeroed(hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, code), device)
+
+
+def hkv_shared_attend_paged(q, K_pool, V_pool, prefix_table, n_prefix: int, page_table, n_own_b, n_own_max: int, out,
+                            lse=None, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, ws=None,
+                            status=None, stream=None) -> None:
+    """Dense decode step of sequences that share their first n_prefix tokens, whose keys and values are read once.
+    q [B, Hq, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; prefix_table [pages],
+    page_table [B, max_pages] and n_own_b [B] int32 (each sequence's own tokens, its query the last of them);
+    out [B, Hq, 128] in q's dtype; lse [B, Hq] fp32."""
+    B, Hq, d = q.shape
+    num_pages, Hkv, page_size, _ = K_pool.shape
+    _need(q, "q", (torch.bfloat16, torch.float32), contiguous=False)
+    _need_rows(q, "q", q.dtype, (B, Hq, 128))
+    _need(K_pool, "K_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
+    _need(V_pool, "V_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
+    _need(prefix_table, "prefix_table", torch.int32)
+    _need(page_table, "page_table", torch.int32)
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be [prefix_pages]")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need(n_own_b, "n_own_b", torch.int32, shape=(B,))
+    _need(out, "out", q.dtype, shape=(B, Hq, 128))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, shape=(B, Hq))
+    sc = _score(softcap, 0, slopes, None, None, B, B, Hq)
+    _here(q, K_pool, V_pool, prefix_table, page_table, n_own_b, out, lse, slopes, ws, status)
+    _ok(lib().hkv_shared_attend_paged(
+        B, Hq, Hkv, _dtype_code(q), _ptr(q), _row_stride(q), _ptr(K_pool), _ptr(V_pool), _ptr(prefix_table),
+        prefix_table.shape[0], n_prefix, _ptr(page_table), page_table.shape[1], num_pages, page_size, _ptr(n_own_b),
+        n_own_max, 1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))

@@ -405,6 +405,177 @@ int hkv_sparse_attend_paged(int B, int Hq, int Hkv, int dtype, const void* q, co
                        static_cast<cudaStream_t>(stream), &pm);
 }
 
+size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv) {
+  if (hash == nullptr || check_hash(hash) != HKV_OK || T < 0 || Hkv < 1) return 0;
+  return append_ws_bytes(hash, T, Hkv);
+}
+
+static int check_dtype(int dtype) {
+  if (dtype != HKV_F32 && dtype != HKV_BF16) return fail(HKV_ERR_INVALID_ARG, "dtype %d", dtype);
+  return HKV_OK;
+}
+
+// Rows of `heads` dense heads, `stride` elements apart, read as 16-byte pieces.
+static int check_rows(const char* name, const void* p, int64_t stride, int heads, int dtype) {
+  if (p == nullptr) return fail(HKV_ERR_INVALID_ARG, "%s is NULL", name);
+  const int64_t elt = dtype == HKV_BF16 ? 2 : 4;
+  if (stride < (int64_t)heads * kHeadDim || !aligned(p, 16) || (stride * elt) % 16 != 0)
+    return fail(HKV_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned and hold %d heads (stride %lld)", name, heads,
+                (long long)stride);
+  return HKV_OK;
+}
+
+int hkv_append_paged(const hkv_hash* hash, int dtype, const hkv_rope* rope, int B, int64_t T, int Hq, int Hkv,
+                     const void* q, int64_t q_stride, void* q_out, int64_t qo_stride, const void* k_new,
+                     int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* cu_new,
+                     const int32_t* n_past, const int32_t* positions, void* K_pool, void* V_pool,
+                     uint32_t* codes_pool, uint16_t* norms_pool, const int32_t* page_table, int64_t max_pages,
+                     int64_t num_pages, int page_size, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  int rc = check_dtype(dtype);
+  if (rc == HKV_OK && hash != nullptr) rc = check_hash(hash);
+  if (rc != HKV_OK) return rc;
+  if (hash != nullptr && hash->dtype != dtype) return fail(HKV_ERR_INVALID_ARG, "hash dtype %d, cache dtype %d", hash->dtype, dtype);
+  if (B < 0 || T < 0 || Hkv < 1 || (q != nullptr && Hq < 1))
+    return fail(HKV_ERR_INVALID_ARG, "B %d T %lld Hq %d Hkv %d", B, (long long)T, Hq, Hkv);
+  if (Hkv > 256 || (q != nullptr && Hq > 4096)) return fail(HKV_ERR_UNSUPPORTED, "Hq %d Hkv %d (at most 4096 and 256)", Hq, Hkv);
+  if (rope != nullptr) {
+    if (rope->pairs < 0 || rope->pairs > kHeadDim / 2 || rope->pairs % 8 != 0)
+      return fail(HKV_ERR_UNSUPPORTED, "rope pairs %d (a multiple of 8 up to 64)", rope->pairs);
+    if (rope->n_axes < 1 || rope->n_axes > 4) return fail(HKV_ERR_UNSUPPORTED, "rope n_axes %d (1..4)", rope->n_axes);
+    if (rope->interleaved != 0 && rope->interleaved != 1) return fail(HKV_ERR_INVALID_ARG, "rope interleaved %d", rope->interleaved);
+    for (int i = 0; i < rope->pairs; ++i)
+      if (rope->axis[i] >= rope->n_axes) return fail(HKV_ERR_INVALID_ARG, "rope axis[%d] is %d of %d", i, rope->axis[i], rope->n_axes);
+    if (rope->pairs > 0 && rope->inv_freq == nullptr) return fail(HKV_ERR_INVALID_ARG, "rope inv_freq is NULL");
+    if (rope->n_axes > 1 && positions == nullptr) return fail(HKV_ERR_INVALID_ARG, "several position axes need positions");
+  }
+  PageMap pm;
+  rc = check_pages(page_table, max_pages, num_pages, page_size, 0, pm);
+  if (rc != HKV_OK) return rc;
+  if (B == 0 || T == 0) return HKV_OK;
+  rc = check_rows("k_new", k_new, k_stride, Hkv, dtype);
+  if (rc == HKV_OK) rc = check_rows("v_new", v_new, v_stride, Hkv, dtype);
+  if (rc == HKV_OK && (q != nullptr || q_out != nullptr)) rc = check_rows("q", q, q_stride, Hq, dtype);
+  if (rc == HKV_OK && q != nullptr) rc = check_rows("q_out", q_out, qo_stride, Hq, dtype);
+  if (rc != HKV_OK) return rc;
+  if (q_out == q && qo_stride != q_stride) return fail(HKV_ERR_INVALID_ARG, "q_out is q with another stride");
+  if (!cu_new || !n_past || !K_pool || !V_pool || !page_table || (hash && !codes_pool))
+    return fail(HKV_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(K_pool, 16) || !aligned(V_pool, 16) || !aligned(codes_pool, 16))
+    return fail(HKV_ERR_INVALID_ARG, "pools must be 16-byte aligned");
+  if (hash && hash->kind == HKV_HASH_LSH && !aligned(hash->R, 16)) return fail(HKV_ERR_INVALID_ARG, "R must be 16-byte aligned");
+  const size_t need = append_ws_bytes(hash, T, Hkv);
+  if (need > 0 && (ws == nullptr || ws_bytes < need))
+    return fail(HKV_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", ws == nullptr ? (size_t)0 : ws_bytes, need);
+  if (need > 0 && !aligned(ws, 256)) return fail(HKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  AppendPaged p{hash, dtype, rope, B, T, Hq, Hkv, q, q_stride, q_out, qo_stride, k_new, k_stride, v_new, v_stride,
+                cu_new, n_past, positions, K_pool, V_pool, codes_pool,
+                hash && hash->kind == HKV_HASH_SIGN ? norms_pool : nullptr, status};
+  return launch_append_paged(p, pm, ws, static_cast<cudaStream_t>(stream));
+}
+
+// What both dense attention calls check; `p` is filled as far as they share it.
+static int check_attend(int B, int64_t T, int Hq, int Hkv, int dtype, float scale, const hkv_score* score,
+                        PagedAttend& p) {
+  int rc = check_heads(B, Hq, Hkv);
+  if (rc == HKV_OK) rc = check_dtype(dtype);
+  if (rc != HKV_OK) return rc;
+  if (T < 0 || T > INT32_MAX) return fail(HKV_ERR_INVALID_ARG, "T %lld", (long long)T);
+  if (Hkv > 65535) return fail(HKV_ERR_UNSUPPORTED, "Hkv %d > 65535", Hkv);
+  if (!std::isfinite(scale)) return fail(HKV_ERR_INVALID_ARG, "scale is not finite");
+  p = PagedAttend{};
+  p.B = B, p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.dtype = dtype, p.scale = scale;
+  if (score != nullptr) {
+    if (!std::isfinite(score->softcap) || score->softcap < 0.f) return fail(HKV_ERR_INVALID_ARG, "softcap %f", (double)score->softcap);
+    if (score->window < 0) return fail(HKV_ERR_INVALID_ARG, "window %d", score->window);
+    p.softcap = score->softcap, p.window = score->window, p.slopes = score->slopes;
+    p.prefix_len = score->prefix_len, p.q_first = score->q_first;
+  }
+  return HKV_OK;
+}
+
+static int check_attend_pools(const PagedAttend& p, const void* ws) {
+  int rc = check_rows("q", p.q, p.q_stride, p.Hq, p.dtype);
+  if (rc != HKV_OK) return rc;
+  if (!p.K_pool || !p.V_pool || !p.out || !p.n_tok) return fail(HKV_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(p.K_pool, 16) || !aligned(p.V_pool, 16) || !aligned(p.out, 16))
+    return fail(HKV_ERR_INVALID_ARG, "K_pool, V_pool and out must be 16-byte aligned");
+  if (!aligned(ws, 256)) return fail(HKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  return HKV_OK;
+}
+
+static int check_prefill(int64_t T, int max_q, int64_t n_max, PagedAttend& p) {
+  if (max_q < 0 || n_max < 0) return fail(HKV_ERR_INVALID_ARG, "max_q %d n_tokens_max %lld", max_q, (long long)n_max);
+  if (n_max > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "n_tokens_max %lld > 2^31-1", (long long)n_max);
+  p.max_q = max_q < T ? max_q : (int)T;
+  p.n_max = n_max;
+  return HKV_OK;
+}
+
+size_t hkv_prefill_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int dtype, int max_q, int64_t n_tokens_max) {
+  PagedAttend p;
+  if (check_attend(B, T, Hq, Hkv, dtype, 1.f, nullptr, p) != HKV_OK || check_prefill(T, max_q, n_tokens_max, p) != HKV_OK)
+    return 0;
+  return B == 0 || p.max_q == 0 ? 0 : attend_paged_ws_bytes(p);
+}
+
+int hkv_prefill_attend_paged(int B, int64_t T, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride,
+                             const void* K_pool, const void* V_pool, const int32_t* page_table, int64_t max_pages,
+                             int64_t num_pages, int page_size, const int32_t* cu_q, const int32_t* n_tokens_b,
+                             int max_q, int64_t n_tokens_max, float scale, const hkv_score* score, void* out,
+                             float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  PagedAttend p;
+  int rc = check_attend(B, T, Hq, Hkv, dtype, scale, score, p);
+  if (rc == HKV_OK) rc = check_prefill(T, max_q, n_tokens_max, p);
+  if (rc == HKV_OK) rc = check_pages(page_table, max_pages, num_pages, page_size, n_tokens_max, p.pm);
+  if (rc != HKV_OK) return rc;
+  if (B == 0 || p.max_q == 0) return HKV_OK;
+  p.q = q, p.q_stride = q_stride, p.K_pool = K_pool, p.V_pool = V_pool, p.cu_q = cu_q, p.n_tok = n_tokens_b;
+  p.out = out, p.lse = lse, p.status = status;
+  rc = check_attend_pools(p, ws);
+  if (rc != HKV_OK) return rc;
+  if (cu_q == nullptr) return fail(HKV_ERR_INVALID_ARG, "cu_q is NULL");
+  return launch_attend_paged(p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+static int check_shared(int64_t n_prefix, int64_t n_own_max, PagedAttend& p) {
+  if (n_prefix < 0 || n_own_max < 0)
+    return fail(HKV_ERR_INVALID_ARG, "n_prefix %lld n_own_max %lld", (long long)n_prefix, (long long)n_own_max);
+  if (n_prefix > INT32_MAX || n_own_max > INT32_MAX || n_prefix + n_own_max > INT32_MAX)
+    return fail(HKV_ERR_UNSUPPORTED, "n_prefix + n_own_max > 2^31-1");
+  p.max_q = 1, p.n_max = n_own_max, p.n_prefix = n_prefix;
+  return HKV_OK;
+}
+
+size_t hkv_shared_workspace_bytes(int B, int Hq, int Hkv, int dtype, int64_t n_prefix, int64_t n_own_max) {
+  PagedAttend p;
+  if (check_attend(B, B, Hq, Hkv, dtype, 1.f, nullptr, p) != HKV_OK || check_shared(n_prefix, n_own_max, p) != HKV_OK)
+    return 0;
+  return B == 0 ? 0 : attend_paged_ws_bytes(p);
+}
+
+int hkv_shared_attend_paged(int B, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride, const void* K_pool,
+                            const void* V_pool, const int32_t* prefix_table, int64_t prefix_pages, int64_t n_prefix,
+                            const int32_t* page_table, int64_t max_pages, int64_t num_pages, int page_size,
+                            const int32_t* n_own_b, int64_t n_own_max, float scale, const hkv_score* score, void* out,
+                            float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream) {
+  PagedAttend p;
+  int rc = check_attend(B, B, Hq, Hkv, dtype, scale, score, p);
+  if (rc == HKV_OK) rc = check_shared(n_prefix, n_own_max, p);
+  if (rc == HKV_OK) rc = check_pages(page_table, max_pages, num_pages, page_size, n_own_max, p.pm);
+  if (rc != HKV_OK) return rc;
+  if (p.window > 0 || p.prefix_len || p.q_first)
+    return fail(HKV_ERR_UNSUPPORTED, "window, prefix_len and q_first have no meaning behind a shared prefix");
+  if (prefix_pages < 0 || prefix_pages * (int64_t)page_size < n_prefix)
+    return fail(HKV_ERR_INVALID_ARG, "prefix_pages * page_size < n_prefix");
+  if (n_prefix > 0 && prefix_table == nullptr) return fail(HKV_ERR_INVALID_ARG, "prefix_table is NULL");
+  if (B == 0) return HKV_OK;
+  p.q = q, p.q_stride = q_stride, p.K_pool = K_pool, p.V_pool = V_pool, p.n_tok = n_own_b;
+  p.prefix_table = prefix_table, p.out = out, p.lse = lse, p.status = status;
+  rc = check_attend_pools(p, ws);
+  if (rc != HKV_OK) return rc;
+  return launch_attend_paged(p, ws, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
 int hkv_lse_merge(int rows, int d, const float* o1, const float* lse1, const float* o2,
                   const float* lse2, float* out, float* lse_out, void* stream) {
   if (rows < 0 || d < 1) return fail(HKV_ERR_INVALID_ARG, "rows %d d %d", rows, d);

@@ -1,0 +1,106 @@
+// What the kernels of the dense attention over a paged cache share: the
+// arguments, which cache positions a query sees, and how a score is formed.
+//
+// A row is one query head of one new token.  Token t of sequence b sits at
+// position p = tokens of b before it + its place among b's new tokens; it sees
+// the positions [lo, hi) of its sequence,
+//   lo = max(0, q_first[t], p + 1 - window),   hi = min(n, max(p + 1, prefix_len[b]))
+// (an interval, whatever the masks), and its scores are
+//   z(u) = cap tanh(scale q.k_u / cap) - slope_h |p - u|.
+// Scores are kept times log2(e), so that every exponential is one exp2.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "internal.h"
+
+namespace hkv {
+namespace pa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Args {
+  int B, Hq, Hkv, g;
+  int64_t T;                  // rows of q, out and lse
+  int max_q;                  // new tokens of a sequence, at most
+  const void* q;
+  int64_t q_stride;
+  const void *K, *V;
+  PageMap pm;
+  const int32_t* cu;          // [B + 1] first new token of each sequence; null: token b is sequence b's only one
+  const int32_t* n_tok;       // [B] tokens in each sequence's own pages
+  int64_t n_max;
+  const int32_t* prefix_table;  // pages of the shared prefix, null without one
+  int64_t n_prefix;             // tokens of the shared prefix
+  int64_t prefix_pages;
+  float scale, softcap;
+  int window;
+  const float* slopes;
+  const int32_t *prefix_len, *q_first;
+  void* out;
+  float* lse;
+  // partials of rows whose positions are split: [part][T * Hq] rows
+  float* part_o;
+  float2* part_ml;            // running maximum (log2 units) and sum
+  uint32_t* tickets;          // zero before and after every call
+  int prefix_parts, own_parts;
+  int32_t* status;
+  uint64_t wait_ns;
+};
+
+// One sequence's new tokens and cache length.
+struct Seq {
+  int64_t first, n_new, n;  // first row of q, number of them, tokens in the sequence's own pages
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b, bool tell) {
+  Seq s;
+  s.first = a.cu ? a.cu[b] : b;
+  s.n_new = a.cu ? a.cu[b + 1] - s.first : 1;
+  s.n = a.n_tok[b];
+  bool bad = false;
+  if (s.first < 0 || s.n_new < 0 || s.first + s.n_new > a.T) bad = true, s.first = 0, s.n_new = 0;
+  if (s.n_new > a.max_q) bad = true, s.n_new = a.max_q;
+  if (s.n < 0) bad = true, s.n = 0;
+  if (s.n > a.n_max) bad = true, s.n = a.n_max;
+  if (bad && tell) report(a.status, HKV_ERR_DEVICE_RANGE);
+  return s;
+}
+
+struct Span {
+  int lo, hi, pos;
+};
+// Positions seen by new token i of sequence b (prefill: the own pages hold the
+// whole sequence).
+__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i) {
+  Span r;
+  // a call may hold more new tokens than the clamped length: positions below
+  // zero see nothing but a prefix
+  const int64_t p = s.n - s.n_new + i;
+  int64_t lo = 0, hi = p + 1;
+  if (a.window > 0 && p + 1 - a.window > lo) lo = p + 1 - a.window;
+  if (a.q_first) {
+    const int64_t f = a.q_first[s.first + i];
+    lo = f > lo ? f : lo;
+  }
+  if (a.prefix_len) {
+    const int64_t f = a.prefix_len[b];
+    hi = f > hi ? f : hi;
+  }
+  hi = hi < s.n ? hi : s.n;
+  hi = hi > 0 ? hi : 0;
+  lo = lo < hi ? lo : hi;
+  r.lo = (int)lo, r.hi = (int)hi, r.pos = (int)p;
+  return r;
+}
+
+// Pool row (of KV head j) that holds token u behind `table`, -1 for a page
+// outside the pool.
+__device__ __forceinline__ int64_t pool_row(const Args& a, const int32_t* __restrict__ table, int64_t u, int j) {
+  const int64_t page = table[u / a.pm.page_size];
+  if (page < 0 || page >= a.pm.num_pages) return -1;
+  return (page * a.Hkv + j) * a.pm.page_size + u % a.pm.page_size;
+}
+
+}  // namespace pa
+}  // namespace hkv

@@ -115,6 +115,58 @@ int launch_lse_merge_n(int G, int64_t rows, const float* o, const float* lse, fl
 int launch_retrieve_paged(const RetrieveShape& s, const PageMap& pm, const uint32_t* q_codes,
                           const uint32_t* codes_pool, int32_t* idx, int32_t* dist, int32_t* status, cudaStream_t st);
 
+// Appending to a paged cache (append_paged.cu).  Strides in elements between
+// tokens; the heads of a token are dense.
+struct AppendPaged {
+  const hkv_hash* hash;  // null: no codes
+  int dtype;
+  const hkv_rope* rope;  // null: nothing is turned
+  int B;
+  int64_t T;
+  int Hq, Hkv;
+  const void* q;         // nullable
+  int64_t q_stride;
+  void* q_out;
+  int64_t qo_stride;
+  const void* k_new;
+  int64_t k_stride;
+  const void* v_new;
+  int64_t v_stride;
+  const int32_t *cu_new, *n_past, *positions;
+  void *K_pool, *V_pool;
+  uint32_t* codes_pool;
+  uint16_t* norms_pool;
+  int32_t* status;
+};
+size_t append_ws_bytes(const hkv_hash* h, int64_t T, int Hkv);
+int launch_append_paged(const AppendPaged& p, const PageMap& pm, void* ws, cudaStream_t st);
+
+// Dense attention over a paged cache (attend_paged.cu): the new tokens of a
+// ragged batch, and the decode step of a batch behind a shared prefix.
+struct PagedAttend {
+  int B, Hq, Hkv, dtype;
+  int64_t T;             // rows of q and out
+  int max_q;             // new tokens of a sequence, at most
+  const void* q;
+  int64_t q_stride;
+  const void *K_pool, *V_pool;
+  PageMap pm;
+  const int32_t* cu_q;   // null: one token a sequence
+  const int32_t* n_tok;
+  int64_t n_max;
+  const int32_t* prefix_table;
+  int64_t n_prefix;
+  float scale, softcap;
+  int window;
+  const float* slopes;
+  const int32_t *prefix_len, *q_first;
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+size_t attend_paged_ws_bytes(const PagedAttend& p);
+int launch_attend_paged(const PagedAttend& p, void* ws, size_t ws_bytes, cudaStream_t st);
+
 // ---- attention (attend.cu) ----
 struct AttendShape {
   int B, Hq, Hkv, dtype;

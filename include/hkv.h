@@ -450,6 +450,141 @@ int hkv_sparse_attend_paged(int B, int Hq, int Hkv, int dtype, const void* q, co
                             int64_t n_tokens, const int32_t* idx, int top_k, int n_sink, int n_local, float scale,
                             float* out, float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream);
 
+/* Rotary positions.  Pair i (0 <= i < pairs) of a head of 128 elements is
+ * (i, i + pairs), or (2 i, 2 i + 1) when interleaved; a token turns it by the
+ * angle position[axis[i]] * inv_freq[i]:
+ *   lo' = lo cos - hi sin,   hi' = hi cos + lo sin
+ * Elements from 2 * pairs on stay as they are.  Angles are taken in fp64, sine
+ * and cosine rounded to fp32, products and sums are fp32 operations.
+ *   pairs        a multiple of 8, 0..64
+ *   interleaved  0 or 1
+ *   n_axes       position axes, 1..4 (one for text; time, height and width for
+ *                pictures and video)
+ *   axis         the position axis of each pair, below n_axes
+ *   inv_freq     device, [pairs] fp32 */
+typedef struct {
+  int32_t pairs;
+  int32_t interleaved;
+  int32_t n_axes;
+  int32_t reserved;
+  const float* inv_freq;
+  uint8_t axis[64];
+} hkv_rope;
+
+/* Appends the new tokens of a ragged batch to a paged cache: keys are turned
+ * by their rotary positions and stored, values are stored, the hash codes (and
+ * norms) of the stored keys go beside them, and the queries, if given, are
+ * turned as well.  New token t (cu_new[b] <= t < cu_new[b + 1]) of sequence b
+ * goes to position n_past[b] + t - cu_new[b] of its page table.
+ *   hash       nullable: no codes are written.  hash->dtype must equal dtype.
+ *              codes_pool (and norms_pool, SIGN only, nullable) get exactly
+ *              what hkv_encode_keys gives for the stored keys
+ *   rope       nullable: nothing is turned
+ *   T          rows of q, k_new and v_new; rows from cu_new[B] on are ignored
+ *   q, q_out   nullable together: [T, Hq, 128] in dtype; q_out may be q (same
+ *              stride).  Row t starts at t * q_stride (qo_stride) elements; the
+ *              heads of a row are dense
+ *   k_new, v_new  [T, Hkv, 128] in dtype, rows at k_stride and v_stride
+ *   cu_new     device int32 [B + 1], ascending from 0;  n_past  device int32 [B]
+ *   positions  device int32 [n_axes, T]; nullable with one axis: a token's
+ *              position is then its position in the cache
+ *   K_pool, V_pool, codes_pool, norms_pool [num_pages, Hkv, page_size], pages
+ *              as above
+ *   ws         hkv_append_paged_workspace_bytes bytes (0 for the bf16 LSH and
+ *              the SIGN hash and without one); no zero fill needed
+ * A position outside the page table or a page id outside the pool is reported
+ * as HKV_ERR_DEVICE_RANGE and the token is not stored.  Two tokens with the
+ * same place in the pool (a page that two sequences both extend) race.  One
+ * launch for the hashes without a workspace, three otherwise. */
+int hkv_append_paged(const hkv_hash* hash, int dtype, const hkv_rope* rope, int B, int64_t T, int Hq, int Hkv,
+                     const void* q, int64_t q_stride, void* q_out, int64_t qo_stride, const void* k_new,
+                     int64_t k_stride, const void* v_new, int64_t v_stride, const int32_t* cu_new,
+                     const int32_t* n_past, const int32_t* positions, void* K_pool, void* V_pool,
+                     uint32_t* codes_pool, uint16_t* norms_pool, const int32_t* page_table, int64_t max_pages,
+                     int64_t num_pages, int page_size, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace that hkv_append_paged needs (0: none). */
+size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv);
+
+/* How the scores of the two attention calls below are formed, and what is
+ * seen.  With the query at position p and the key at position u of a sequence,
+ *   z(u) = cap(scale * q.k_u) - slopes[h] * |p - u|,
+ *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0
+ * and query row t sees the positions u with
+ *   max(0, q_first[t], p + 1 - window) <= u < min(n, max(p + 1, prefix_len[b])).
+ *   softcap     >= 0
+ *   window      >= 0; 0: no window
+ *   slopes      nullable, device fp32 [Hq]
+ *   prefix_len  nullable, device int32 [B]: the first prefix_len[b] positions
+ *               are seen by every query of the sequence (as far as the window
+ *               and q_first let them), also by the earlier ones
+ *   q_first     nullable, device int32 [T]: the first position that a query
+ *               sees, e.g. the start of its document
+ * Keys that a query does not see may hold anything.  Values must be finite at
+ * every position below n: one that some query of the sequence sees is also
+ * multiplied, by zero, for the others. */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* slopes;
+  const int32_t* prefix_len;
+  const int32_t* q_first;
+} hkv_score;
+
+/* Attention of the new tokens of a ragged batch over their paged caches, new
+ * tokens included (append them first).  Sequence b has n_tokens_b[b] = n
+ * tokens in its pages; its new tokens, rows cu_q[b] .. cu_q[b + 1] of q, are
+ * the last ones, so that new token i sits at position
+ * p = n - (cu_q[b + 1] - cu_q[b]) + i.
+ *   out[t, h] = sum_u softmax_u(z(u)) V[u],   lse[t, h] = log sum_u exp z(u)
+ * over the positions u that the row sees (hkv_score); a row that sees nothing
+ * gets 0 and -inf.  With one new token a sequence this is the dense decode step.
+ *   q        [T, Hq, 128] in dtype (HKV_BF16 or HKV_F32), rows at q_stride
+ *            elements, 16-byte aligned;  T rows, those from cu_q[B] on are
+ *            ignored and their out and lse rows left as they are
+ *   cu_q     device int32 [B + 1], ascending from 0;  n_tokens_b device int32 [B]
+ *   max_q, n_tokens_max   upper bounds of a sequence's new tokens and tokens;
+ *            they plan the launch and size the workspace.  A sequence past
+ *            them is cut to them and reported as HKV_ERR_DEVICE_RANGE
+ *   score    nullable: plain causal attention
+ *   out      [T, Hq, 128] in dtype;  lse nullable [T, Hq] fp32
+ *   ws       hkv_prefill_workspace_bytes bytes, zeroed once before its first
+ *            use (hkv_workspace_reset) and returned to that state by every
+ *            call; the rules of hkv_workspace_bytes on sharing and other
+ *            shapes hold.  A page id outside the pool is reported as
+ * HKV_ERR_DEVICE_RANGE and its tokens are not attended. */
+int hkv_prefill_attend_paged(int B, int64_t T, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride,
+                             const void* K_pool, const void* V_pool, const int32_t* page_table, int64_t max_pages,
+                             int64_t num_pages, int page_size, const int32_t* cu_q, const int32_t* n_tokens_b,
+                             int max_q, int64_t n_tokens_max, float scale, const hkv_score* score, void* out,
+                             float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
+size_t hkv_prefill_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int dtype, int max_q, int64_t n_tokens_max);
+
+/* Dense decode step of a batch of sequences that share their first n_prefix
+ * tokens.  The prefix's keys and values are read once for the whole batch: the
+ * query heads of all sequences meet them together, and the result is joined
+ * with each sequence's own tokens by log-sum-exp rescaling.
+ * Sequence b is the prefix, in the pages prefix_table[0 ..], then its own
+ * n_own_b[b] tokens, in the pages page_table[b, 0 ..] of the same pools (its own
+ * tokens start on a page of their own; the prefix may end inside a page).  Its
+ * query is the last of them, at position n_prefix + n_own_b[b] - 1, and sees all.
+ *   q         [B, Hq, 128] in dtype, rows at q_stride elements, 16-byte aligned
+ *   prefix_table  device int32 [prefix_pages], prefix_pages * page_size >= n_prefix
+ *   page_table    device int32 [B, max_pages]
+ *   n_own_b   device int32 [B], each in [0, n_own_max]; others are cut to that
+ *             and reported as HKV_ERR_DEVICE_RANGE
+ *   score     nullable; softcap and slopes only (HKV_ERR_UNSUPPORTED otherwise)
+ *   out       [B, Hq, 128] in dtype;  lse nullable [B, Hq] fp32
+ *   ws        hkv_shared_workspace_bytes bytes, zeroed once, as above */
+int hkv_shared_attend_paged(int B, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride, const void* K_pool,
+                            const void* V_pool, const int32_t* prefix_table, int64_t prefix_pages, int64_t n_prefix,
+                            const int32_t* page_table, int64_t max_pages, int64_t num_pages, int page_size,
+                            const int32_t* n_own_b, int64_t n_own_max, float scale, const hkv_score* score, void* out,
+                            float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
+size_t hkv_shared_workspace_bytes(int B, int Hq, int Hkv, int dtype, int64_t n_prefix, int64_t n_own_max);
+
 /* Elementwise log-sum-exp merge of two partial attention results (S8 alone).
  * RetrievalAttention "Approach".  For each of `rows` rows:
  *   m = max(lse1, lse2), w_i = exp(lse_i - m)

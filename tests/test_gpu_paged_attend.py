@@ -1,0 +1,328 @@
+"""Dense attention over a paged cache: ragged prompts, single tokens, capped scores, bias by distance, window, document
+and prefix masks, and sequences behind a shared prefix, against the 64-bit statement."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import hash_sparse_kv_b200 as hkv
+from tests.paged_plain import D, attend, check, scatter, score_error, spans
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _i(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def _prompt(dt, Hq, Hkv, P, new, total, softcap=0.0, window=0, slopes=False, prefix=None, docs=0, scale=None, spread=1.5,
+            behind=2, strided=False, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    B, T = len(new), sum(new) + behind
+    Ks = [torch.randn(n, Hkv, D, generator=g).to(dt) for n in total]
+    Vs = [(torch.randn(n, Hkv, D, generator=g) + 0.5).to(dt) for n in total]
+    g2 = torch.Generator().manual_seed(seed + 1)
+    kpool, table = scatter(Ks, P, g2)
+    g2.manual_seed(seed + 1)
+    vpool, _ = scatter(Vs, P, g2)
+    q = (torch.randn(T, Hq, D, generator=g) * spread).to(dt)
+    sl = 2.0 ** (-8 * torch.arange(1, Hq + 1) / Hq) if slopes else None
+    first = None
+    if docs:
+        first = torch.cat([torch.arange(n - m, n) // docs * docs for m, n in zip(new, total)] + [torch.zeros(behind)]).int()
+    qd = q.to(DEV)
+    if strided:
+        qd = torch.cat([qd, qd, qd], 1)[:, Hq:2 * Hq]
+    out = torch.full((T, Hq, D), 9.0, dtype=dt, device=DEV)
+    lse = torch.full((T, Hq), 9.0, device=DEV)
+    st = hkv.status_word()
+    mq, mn = max(new), max(total)
+    ws = hkv.prefill_workspace(B, Hq, Hkv, T, mq, mn, dt)
+    args = (qd, kpool.to(DEV), vpool.to(DEV), table.to(DEV), _i([0] + list(itertools.accumulate(new))), _i(total), mq, mn)
+    kw = dict(scale=scale, softcap=softcap, window=window, slopes=None if sl is None else sl.to(DEV),
+              prefix_len=None if prefix is None else _i(prefix), q_first=None if first is None else first.to(DEV), ws=ws,
+              status=st)
+    for again in range(2):  # the second call finds the workspace as the first left it
+        out.fill_(9.0), lse.fill_(9.0)
+        hkv.hkv_prefill_attend_paged(*args, out, lse=lse, **kw)
+        assert hkv.hkv_check(st) == hkv.HKV_OK, hkv.hkv_last_error()
+        if not again:
+            kept = out.clone(), lse.clone()
+    assert torch.equal(kept[0], out) and torch.equal(kept[1], lse)
+    at, s = 0, 1 / math.sqrt(D) if scale is None else scale
+    o, l = out.cpu(), lse.cpu()
+    for b, (m, n) in enumerate(zip(new, total)):
+        pos, lo, hi = spans(n, m, window, 0 if prefix is None else prefix[b], None if first is None else first[at:at + m])
+        want = attend(q[at:at + m], Ks[b], Vs[b], pos, lo, hi, s, softcap, sl)
+        if m:
+            dz = score_error(q[at:at + m], Ks[b], s)
+            if sl is not None:
+                dz += 2.0 ** -23 * float(sl.max()) * n
+            check(o[at:at + m], l[at:at + m], want, dt, dz, n)
+        at += m
+    assert (o[at:] == 9).all() and (l[at:] == 9).all()
+
+
+PROMPTS = [
+    # dtype, Hq, Hkv, page, new, total, options
+    (BF, 4, 2, 16, [1], [1], {}),
+    (BF, 4, 1, 16, [3, 1, 2], [3, 1, 40], {}),
+    (BF, 28, 4, 64, [130, 0, 77], [130, 50, 500], {}),
+    (BF, 8, 2, 48, [257, 31], [700, 31], dict(strided=True)),
+    (BF, 8, 8, 5, [33, 129], [170, 129], {}),
+    (BF, 16, 1, 1, [17, 40], [17, 95], {}),
+    (BF, 4, 4, 100, [300], [1333], dict(softcap=20.0, spread=4.0)),
+    (BF, 14, 2, 256, [90, 300], [900, 301], dict(softcap=5.0, window=64, spread=4.0)),
+    (BF, 6, 2, 16, [200, 64], [200, 300], dict(slopes=True)),
+    (BF, 8, 2, 32, [150, 200], [150, 520], dict(window=1)),
+    (BF, 8, 2, 8, [150, 200], [150, 520], dict(window=131, slopes=True)),
+    (BF, 4, 2, 24, [300, 260], [310, 700], dict(docs=37)),
+    (BF, 4, 2, 128, [300, 260], [310, 700], dict(prefix=[250, 1000])),
+    (BF, 4, 1, 64, [300, 260], [310, 700], dict(prefix=[64, 0], docs=100, window=150, slopes=True, softcap=30.0)),
+    (BF, 4, 4, 16, [64, 64], [40, 64], {}),   # more new tokens than the cache holds: the first rows see nothing
+    (BF, 12, 4, 64, [9], [3000], {}),        # few rows, long past
+    (BF, 32, 8, 64, [40], [9000], {}),       # few rows over many pages: split
+    (BF, 4, 2, 16, [120], [120], dict(scale=0.0)),
+    (BF, 4, 2, 16, [120], [400], dict(scale=1.0, spread=1.0)),   # scores of tens: one key takes nearly all
+    (F32, 8, 2, 5, [37, 1, 0, 12], [300, 1, 4, 12], {}),
+    (F32, 4, 4, 64, [70], [500], dict(softcap=10.0, window=100, slopes=True, spread=3.0)),
+    (F32, 16, 1, 16, [9, 20], [9, 90], dict(prefix=[6, 80], docs=11)),
+    (F32, 7, 1, 16, [5], [4000], {}),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_prompt(case):
+    dt, Hq, Hkv, P, new, total, kw = PROMPTS[case]
+    _prompt(dt, Hq, Hkv, P, new, total, seed=100 + case, **kw)
+
+
+SINGLE = [
+    (BF, 32, 8, 64, [1, 17, 64, 300, 1025, 0], {}),
+    (BF, 28, 4, 16, [5000], {}),
+    (BF, 16, 1, 48, [1, 2, 3, 700], dict(softcap=15.0, slopes=True, spread=4.0)),
+    (BF, 4, 4, 5, [33, 800, 90], dict(window=40)),
+    (BF, 8, 2, 256, [3000] * 9, dict(docs=700)),
+    (BF, 8, 8, 1, [40, 41], {}),
+    (F32, 8, 2, 64, [1, 30, 2000], dict(softcap=15.0)),
+    (F32, 2, 2, 7, [77, 0, 5], dict(window=3)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SINGLE)))
+def test_single_tokens(case):
+    dt, Hq, Hkv, P, total, kw = SINGLE[case]
+    _prompt(dt, Hq, Hkv, P, [1] * len(total), total, seed=300 + case, **kw)
+
+
+def _shared(dt, Hq, Hkv, P, n_prefix, own, softcap=0.0, slopes=False, spread=1.5, strided=False, seed=0, behind=0):
+    g = torch.Generator().manual_seed(seed)
+    B = len(own)
+    Kp, Vp = (torch.randn(n_prefix, Hkv, D, generator=g).to(dt) for _ in range(2))
+    Ks, Vs = ([torch.randn(n, Hkv, D, generator=g).to(dt) for n in own] for _ in range(2))
+    g2 = torch.Generator().manual_seed(seed + 1)
+    kpool, table = scatter([Kp] + Ks, P, g2)
+    g2.manual_seed(seed + 1)
+    vpool, _ = scatter([Vp] + Vs, P, g2)
+    q = (torch.randn(B, Hq, D, generator=g) * spread).to(dt)
+    sl = 2.0 ** (-8 * torch.arange(1, Hq + 1) / Hq) if slopes else None
+    qd = q.to(DEV)
+    if strided:
+        qd = torch.cat([qd, qd], 1)[:, Hq:]
+    out = torch.full((B, Hq, D), 9.0, dtype=dt, device=DEV)
+    lse = torch.full((B, Hq), 9.0, device=DEV)
+    st = hkv.status_word()
+    ws = hkv.shared_workspace(B, Hq, Hkv, n_prefix, max(own), dt)
+    for again in range(2):
+        out.fill_(9.0), lse.fill_(9.0)
+        hkv.hkv_shared_attend_paged(qd, kpool.to(DEV), vpool.to(DEV), table[0].to(DEV), n_prefix, table[1:].contiguous().to(DEV),
+                                    _i(own), max(own), out, lse=lse, softcap=softcap,
+                                    slopes=None if sl is None else sl.to(DEV), ws=ws, status=st)
+        assert hkv.hkv_check(st) == hkv.HKV_OK, hkv.hkv_last_error()
+        if not again:
+            kept = out.clone(), lse.clone()
+    assert torch.equal(kept[0], out) and torch.equal(kept[1], lse)
+    for b, n in enumerate(own):
+        K, V = torch.cat([Kp, Ks[b]]), torch.cat([Vp, Vs[b]])
+        m = n_prefix + n
+        want = attend(q[b:b + 1], K, V, torch.tensor([m - 1]), torch.tensor([0]), torch.tensor([m]), 1 / math.sqrt(D), softcap, sl)
+        dz = score_error(q[b:b + 1], K, 1 / math.sqrt(D)) + (2.0 ** -23 * float(sl.max()) * m if slopes else 0.0)
+        check(out[b:b + 1].cpu(), lse[b:b + 1].cpu(), want, dt, dz, m)
+
+
+SHARED = [
+    (BF, 4, 2, 16, 100, [1, 5, 0, 33], {}),
+    (BF, 28, 4, 64, 1000, [70] * 9, {}),
+    (BF, 32, 8, 64, 4096, [1, 600, 64, 65, 3], dict(strided=True)),
+    (BF, 8, 2, 48, 777, list(range(1, 71)), {}),
+    (BF, 8, 8, 5, 203, [9, 10], dict(softcap=10.0, spread=4.0)),
+    (BF, 16, 1, 256, 3000, [4, 500, 90], dict(slopes=True)),
+    (BF, 8, 2, 16, 0, [5, 0, 40], {}),          # no prefix, and a sequence without any token
+    (BF, 8, 2, 16, 129, [0, 0], {}),            # nothing of their own
+    (BF, 2, 2, 1, 131, [3] * 200, {}),
+    (BF, 4, 1, 64, 20000, [2], dict(softcap=30.0, slopes=True)),
+    (F32, 8, 2, 16, 300, [5, 0, 77], {}),
+    (F32, 3, 1, 7, 1500, [1] * 20, dict(softcap=10.0, slopes=True, spread=3.0)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_shared_prefix(case):
+    dt, Hq, Hkv, P, n_prefix, own, kw = SHARED[case]
+    _shared(dt, Hq, Hkv, P, n_prefix, own, seed=500 + case, **kw)
+
+
+def _cache(B, n, Hkv=2, P=16, dt=BF, seed=3):
+    g = torch.Generator().manual_seed(seed)
+    toks = [torch.randn(n, Hkv, D, generator=g).to(dt) for _ in range(B)]
+    pool, table = scatter(toks, P, g)
+    return toks, pool.to(DEV), table.to(DEV)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+def test_a_page_outside_the_pool_is_reported_and_not_attended(new):
+    n, P, Hq = 200, 16, 4
+    toks, pool, table = _cache(1, n)
+    table[0, 2] = pool.shape[0]  # tokens 32..47
+    q = torch.randn(new, Hq, D, device=DEV).to(BF)
+    out, lse, st = torch.zeros(new, Hq, D, dtype=BF, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q, pool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, status=st,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n))
+    assert hkv.hkv_check(st) == hkv.HKV_ERR_DEVICE_RANGE
+    keep = torch.cat([torch.arange(32), torch.arange(48, n)])
+    pos = torch.arange(n - new, n)
+    hi = torch.tensor([int((keep <= p).sum()) for p in pos])
+    K = toks[0][keep]
+    want = attend(q.cpu(), K, K, pos, torch.zeros_like(hi), hi, 1 / math.sqrt(D))
+    check(out.cpu(), lse.cpu(), want, BF, score_error(q.cpu(), K, 1 / math.sqrt(D)), n)
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_lengths_past_their_bounds_are_cut_and_reported(new):
+    n, Hq = 200, 4
+    toks, pool, table = _cache(1, n)
+    q = torch.randn(new, Hq, D, device=DEV).to(BF)
+    out, st = torch.zeros(new, Hq, D, dtype=BF, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q, pool, pool, table, _i([0, new]), _i([n + 1]), new, n, out, status=st,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n))
+    assert hkv.hkv_check(st) == hkv.HKV_ERR_DEVICE_RANGE
+    pos, lo, hi = spans(n, new)
+    want = attend(q.cpu(), toks[0], toks[0], pos, lo, hi, 1 / math.sqrt(D))
+    check(out.cpu(), want[1].float(), want, BF, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), n)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_masked_keys_may_hold_anything(new):
+    """Keys behind the document's start and behind the last token: NaN and infinities stay out of the result."""
+    n, P, Hq = 330, 16, 4
+    toks, pool, table = _cache(1, n)
+    vpool = pool.nan_to_num(0.0)
+    first = 101
+    flat = toks[0].clone()
+    flat[:first] = float("nan")
+    flat[50] = float("inf")
+    kpool, _ = scatter([flat], P, torch.Generator().manual_seed(0), fill=float("inf"))
+    order = table[0, :-(-n // P)].long().cpu()
+    kp = torch.full_like(pool, float("nan"))
+    vt = torch.zeros_like(vpool)
+    for i, page in enumerate(order):
+        rows = flat[i * P:(i + 1) * P]
+        kp[page, :, :len(rows)] = rows.transpose(0, 1).to(DEV)
+        vt[page] = vpool[page]
+        vt[page, :, len(rows):] = float("nan")
+    q = torch.randn(new, Hq, D, device=DEV).to(BF)
+    out, lse, st = torch.zeros(new, Hq, D, dtype=BF, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q, kp, vt, table, _i([0, new]), _i([n]), new, n, out, lse=lse, status=st,
+                                 q_first=torch.full((new,), first, dtype=torch.int32, device=DEV),
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n))
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    pos, lo, hi = spans(n, new, first=torch.full((new,), first))
+    want = attend(q.cpu(), flat.nan_to_num(0.0, 0.0, 0.0), toks[0], pos, lo, hi, 1 / math.sqrt(D))
+    check(out.cpu(), lse.cpu(), want, BF, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), n)
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_captured_and_replayed_on_a_side_stream(new):
+    """A captured call follows new queries and lengths in its buffers, and equals the eager call bit for bit."""
+    B, n, Hq = 3, 700, 8
+    toks, pool, table = _cache(B, n)
+    q = torch.randn(B * new, Hq, D, device=DEV).to(BF)
+    cu, total = _i([0, new, 2 * new, 3 * new]), _i([n - 5, n, 300])
+    out, lse = torch.zeros(B * new, Hq, D, dtype=BF, device=DEV), torch.zeros(B * new, Hq, device=DEV)
+    ws = hkv.prefill_workspace(B, Hq, 2, B * new, new, n)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call = lambda o, l: hkv.hkv_prefill_attend_paged(q, pool, pool, table, cu, total, new, n, o, lse=l, ws=ws)  # noqa: E731
+        call(out, lse)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call(out, lse)
+    torch.cuda.current_stream().wait_stream(side)
+    q.copy_(torch.randn_like(q))
+    total.copy_(_i([n, 250, n - 1]))
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    call(o2, l2)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_from_prompt_to_retrieval():
+    """The calls in the order of a serving loop: prompts appended (rotary positions, codes) and attended, then single
+    tokens appended and attended densely, behind a shared prefix, and by retrieval that keeps every token resident:
+    the three decode steps agree."""
+    B, Hq, Hkv, P, n = 2, 8, 2, 16, 150
+    g = torch.Generator().manual_seed(8)
+    R = torch.randn(128, D, generator=g).to(BF).to(DEV)
+    h = hkv.HashParams.lsh(R)
+    rope = hkv.RopeParams((1e4 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().to(DEV))
+    pages = -(-(n + 1) // P)
+    K, V = (torch.zeros(2 * pages + 1, Hkv, P, D, dtype=BF, device=DEV) for _ in range(2))
+    codes = torch.zeros(2 * pages + 1, Hkv, P, 4, dtype=torch.int32, device=DEV)
+    table = torch.randperm(2 * pages + 1, generator=g)[:2 * pages].view(2, pages).int().to(DEV)
+    st = hkv.status_word()
+
+    def step(new, past):
+        T = B * new
+        x = torch.randn(T, Hq + 2 * Hkv, D, generator=g).to(BF).to(DEV)
+        q = torch.empty(T, Hq, D, dtype=BF, device=DEV)
+        cu = _i([0, new, 2 * new])
+        hkv.hkv_append_paged(h, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], K, V, table, cu, _i([past] * B), codes, rope=rope, q=x[:, :Hq],
+                             q_out=q, status=st)
+        out, lse = torch.empty_like(q), torch.empty(T, Hq, device=DEV)
+        hkv.hkv_prefill_attend_paged(q, K, V, table, cu, _i([past + new] * B), new, past + new, out, lse=lse, status=st,
+                                     ws=hkv.prefill_workspace(B, Hq, Hkv, T, new, past + new))
+        return x, q, out, lse
+
+    x, q, out, lse = step(n, 0)
+    rows = lambda pool, b, m: pool[table[b].long()].transpose(1, 2).reshape(-1, Hkv, D)[:m].cpu()  # noqa: E731
+    for b in range(B):
+        pos, lo, hi = spans(n, n)
+        Kb = rows(K, b, n)
+        want = attend(q[b * n:(b + 1) * n].cpu(), Kb, x[b * n:(b + 1) * n, Hq + Hkv:].cpu(), pos, lo, hi, 1 / math.sqrt(D))
+        check(out[b * n:(b + 1) * n].cpu(), lse[b * n:(b + 1) * n].cpu(), want, BF, score_error(q.cpu(), Kb, 1 / math.sqrt(D)), n)
+    x, q, out, lse = step(1, n)
+    assert hkv.hkv_check(st) == hkv.HKV_OK, hkv.hkv_last_error()
+    m = n + 1
+    full = torch.empty(B, Hq, D, device=DEV)
+    lse2 = torch.empty(B, Hq, device=DEV)
+    ws = hkv.workspace(B, Hq, Hkv, m, 128, 8, 4, m)
+    hkv.hkv_decode_step_paged(h, q, codes, K, V, table, m, 4, m, 8, full, lse=lse2, ws=ws, status=st)
+    # sequence 0 again, its first two pages as the shared prefix of a batch of one
+    own = m - 2 * P
+    out3, lse3 = torch.empty(1, Hq, D, dtype=BF, device=DEV), torch.empty(1, Hq, device=DEV)
+    hkv.hkv_shared_attend_paged(q[:1], K, V, table[0, :2].contiguous(), 2 * P, table[:1, 2:].contiguous(), _i([own]), own, out3,
+                                lse=lse3, ws=hkv.shared_workspace(1, Hq, Hkv, 2 * P, own), status=st)
+    assert hkv.hkv_check(st) == hkv.HKV_OK, hkv.hkv_last_error()
+    for b in range(B):
+        want = attend(q[b:b + 1].cpu(), rows(K, b, m), rows(V, b, m), torch.tensor([n]), torch.tensor([0]), torch.tensor([m]), 1 / math.sqrt(D))
+        dz = score_error(q[b:b + 1].cpu(), rows(K, b, m), 1 / math.sqrt(D))
+        check(out[b:b + 1].cpu(), lse[b:b + 1].cpu(), want, BF, dz, m)
+        assert (full[b].cpu().double() - want[0][0]).abs().max() < 2e-3 and (lse2[b].cpu().double() - want[1][0]).abs().max() < 2e-3
+        if b == 0:
+            check(out3.cpu(), lse3.cpu(), want, BF, dz, m)
