@@ -506,6 +506,7 @@ static int check_attend_pools(const PagedAttend& p, const void* ws) {
 static int check_prefill(int64_t T, int max_q, int64_t n_max, PagedAttend& p) {
   if (max_q < 0 || n_max < 0) return fail(HKV_ERR_INVALID_ARG, "max_q %d n_tokens_max %lld", max_q, (long long)n_max);
   if (n_max > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "n_tokens_max %lld > 2^31-1", (long long)n_max);
+  p.cu_q_rows = true;
   p.max_q = max_q < T ? max_q : (int)T;
   p.n_max = n_max;
   return HKV_OK;

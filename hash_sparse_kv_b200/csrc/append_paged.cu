@@ -19,7 +19,7 @@
 // per key are far below what the key's own traffic allows).
 #include <cstdio>
 
-#include "internal.h"
+#include "attend_paged.cuh"
 
 namespace hkv {
 namespace {
@@ -49,23 +49,6 @@ struct AppendArgs {
   int32_t* status;
   uint8_t axis[64];
 };
-
-// Sequence of token t: the largest b in [0, B) with cu[b] <= t, found by the
-// whole warp, 32 candidates a round.
-__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int B, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int b = lo + lane * step;
-    const bool le = lane * step < n && (lane == 0 || (int64_t)__ldg(cu + b) <= t);
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    const int last = 31 - __clz(m);  // bit 0 is always set
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return lo;
-}
 
 struct Chunk {
   float x[8];
@@ -166,7 +149,7 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
     __syncthreads();  // the last step's angles, slots and keys have been used
     if (warp < nt) {
       const int64_t t = t0 + warp;
-      const int b = find_seq(a.cu, a.B, t);
+      const int b = pa::find_seq(a.cu, a.B, t);
       if (lane == 0) {
         const int64_t first = a.cu[b], end = a.cu[b + 1];
         int64_t row = -1;
@@ -327,7 +310,7 @@ scatter_codes_kernel(const __grid_constant__ AppendArgs a, const uint32_t* __res
     // a warp's rows belong to few tokens: find each one's sequence together
     const int64_t t_lo = w0 / a.Hkv, t_hi = min(n - 1, w0 + 31) / a.Hkv;
     for (int64_t t = t_lo; t <= t_hi; ++t) {
-      const int b = find_seq(a.cu, a.B, t);
+      const int b = pa::find_seq(a.cu, a.B, t);
       if (i >= n || i / a.Hkv != t) continue;
       const int64_t first = a.cu[b], end = a.cu[b + 1], pos = (int64_t)a.n_past[b] + t - first;
       if (t < first || t >= end || pos < 0 || pos >= a.pm.max_pages * a.pm.page_size) continue;

@@ -110,6 +110,7 @@ __device__ void finish(const Args& a, const Item& it, const float (&acc)[8], con
       }
       for (int p = 0; p < from_memory; ++p) {
         const float2 ml = __ldcg(&a.part_ml[p * n_rows + row]);
+        if (ml.x == -INFINITY) continue;  // an empty part's values need not be written
         const float w = exp2f(ml.x - M);
         L = fmaf(w, ml.y, L);
         o = fmaf(w, __ldcg(&a.part_o[(p * n_rows + row) * kHeadDim + col]), o);
@@ -237,28 +238,45 @@ int splits_for(int64_t items, int64_t tokens, int tile) {
 // How a call is cut up; from its shape and the device alone, so that the
 // workspace can be sized before the call.
 struct Plan {
+  bool tc = false;         // prompts: the tensor-core kernel takes all rows
+  bool tc_prefix = false;  // it takes the shared prefix
   int64_t own_items = 0;
   int prefix_parts = 0, own_parts = 1;
-  size_t tickets = 0, ml = 0, total = 0;  // byte offsets of part_ml and part_o, and the size
+  size_t ml = 0, o = 0, total = 0;  // byte offsets of part_ml and part_o, and the size
 };
 
 Plan plan(const PagedAttend& p) {
   Plan r;
   const int g = p.Hq / p.Hkv, tpt = kRows / g;
-  r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt);
-  r.own_parts = splits_for(r.own_items * p.Hkv, p.n_max, kTile);
-  if (p.n_prefix > 0) r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix, kTile);
-  const int64_t parts = r.prefix_parts + (r.own_parts > 1 ? r.own_parts : 0);
-  r.tickets = align_up(sizeof(uint32_t) * r.own_items * p.Hkv, 256);
-  const size_t ml = align_up(sizeof(float2) * parts * p.T * p.Hq, 256);
-  r.ml = r.tickets;
-  r.total = parts ? r.tickets + ml + sizeof(float) * kHeadDim * parts * p.T * p.Hq : 0;
+  const bool bf16 = p.dtype == HKV_BF16;
+  int64_t parts = 0;
+  // a sequence's new tokens fill more than the 16 rows of one block: 128-row tiles
+  r.tc = bf16 && p.cu_q_rows && (int64_t)p.max_q * g > kRows;
+  if (r.tc) {
+    r.own_parts = tc_splits(p, false);
+  } else {
+    r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt);
+    r.own_parts = splits_for(r.own_items * p.Hkv, p.n_max, kTile);
+    r.tc_prefix = bf16 && p.n_prefix > 0;
+    if (r.tc_prefix)
+      r.prefix_parts = tc_splits(p, true);
+    else if (p.n_prefix > 0)
+      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix, kTile);
+  }
+  parts = r.prefix_parts + (r.own_parts > 1 ? r.own_parts : 0);
+  r.ml = align_up(sizeof(uint32_t) * r.own_items * p.Hkv, 256);
+  r.o = r.ml + align_up(sizeof(float2) * parts * p.T * p.Hq, 256);
+  r.total = parts ? r.o + sizeof(float) * kHeadDim * parts * p.T * p.Hq : 0;
   return r;
 }
 
 template <typename T>
 int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
-  if (pl.prefix_parts > 0) {
+  if (pl.tc) return launch_attend_tc(p, a, false, pl.own_parts, pl.own_parts > 1 ? 0 : -1, st);
+  if (pl.tc_prefix) {
+    const int rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
+    if (rc != HKV_OK) return rc;
+  } else if (pl.prefix_parts > 0) {
     const dim3 grid((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts);
     rows_simt_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
     const int rc = cuda_check(cudaGetLastError(), "prefix attention launch");
@@ -287,10 +305,9 @@ int launch_attend_paged(const PagedAttend& p, void* ws, size_t ws_bytes, cudaStr
   a.wait_ns = wait_limit_ns();
   a.prefix_parts = pl.prefix_parts, a.own_parts = pl.own_parts;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  const int64_t parts = pl.prefix_parts + (pl.own_parts > 1 ? pl.own_parts : 0);
   a.tickets = reinterpret_cast<uint32_t*>(w);
   a.part_ml = reinterpret_cast<float2*>(w + pl.ml);
-  a.part_o = reinterpret_cast<float*>(w + pl.ml + align_up(sizeof(float2) * parts * p.T * p.Hq, 256));
+  a.part_o = reinterpret_cast<float*>(w + pl.o);
   return p.dtype == HKV_BF16 ? run<__nv_bfloat16>(p, pl, a, st) : run<float>(p, pl, a, st);
 }
 

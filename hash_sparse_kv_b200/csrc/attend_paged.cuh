@@ -102,5 +102,28 @@ __device__ __forceinline__ int64_t pool_row(const Args& a, const int32_t* __rest
   return (page * a.Hkv + j) * a.pm.page_size + u % a.pm.page_size;
 }
 
+// Sequence of row t: the largest b in [0, B) with cu[b] <= t, found by the
+// whole warp, 32 candidates a round.
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int B, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int b = lo + lane * step;
+    const bool le = lane * step < n && (lane == 0 || (int64_t)__ldg(cu + b) <= t);
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int last = 31 - __clz(m);  // bit 0 is always set
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
 }  // namespace pa
+
+// The tensor-core kernel (attend_paged_tc.cu): row tiles, splits, launch.
+int64_t tc_tiles(const PagedAttend& p, bool prefix);
+int tc_splits(const PagedAttend& p, bool prefix);
+int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int splits, int part0, cudaStream_t st);
+
 }  // namespace hkv

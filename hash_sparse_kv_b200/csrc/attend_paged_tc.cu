@@ -1,0 +1,653 @@
+// Dense attention over a paged cache on the tensor cores (bf16): prompts and
+// chunks of prompts, and the query heads of a whole batch over a shared prefix.
+//
+// A CTA owns up to 256 rows (query heads of new tokens) of one KV head, two
+// slots of 128, and walks its positions in tiles of 128 tokens:
+//   S = Q K^T         tcgen05.mma, bf16 x bf16 -> fp32 in tensor memory
+//   P = exp2(S - m)   one thread per row: running maximum m, sum l in fp32, P
+//                     rounded to bf16 (one rounding of 2^-9 beside the output's
+//                     own) and written over S in tensor memory
+//   O += P V          tcgen05.mma with P read from tensor memory, fp32 sums
+// The two slots share every K and V tile, so a tile is read once for 256 rows,
+// and one slot's softmax runs while the tensor cores work for the other.  O is
+// rescaled only when a row's maximum has grown by more than 2^8 (until then
+// the old one keeps every exponential within fp32 and bf16 range), which after
+// the first tiles is rare, so the softmax threads do it themselves.
+// With at most 128 rows both slots take the same rows and every other tile.
+//
+// Warps 0-3 and 4-7: softmax of slot 0 and 1; 8: K tiles, 9: V tiles (TMA boxes
+// of as many tokens as a page's size allows, or plain loads where a page ends
+// inside a swizzle group, at the end of the sequence and at bad pages);
+// 10 and 11: the MMAs of slot 0 and 1.
+#include <cstdio>
+#include <mutex>
+
+#include "attend_paged.cuh"
+#include "tc.cuh"
+
+namespace hkv {
+namespace {
+
+using pa::Args;
+
+constexpr int kThreads = 384;
+constexpr int kTile = 128;                  // tokens per tile, rows per slot
+constexpr int kKStages = 3, kVStages = 2;
+constexpr uint32_t kHalf = kTile * 128;     // 128 rows x 64 bf16
+constexpr uint32_t kBuf = 2 * kHalf;
+constexpr int kMaskRing = 8;                // tiles whose valid-token masks are kept
+constexpr float kGrowth = 8.f;              // rescale when the maximum grows by more than 2^8
+
+struct Layout {
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kBuf;
+  static constexpr uint32_t kV = kK + kKStages * kBuf;
+  static constexpr uint32_t kMask = kV + kVStages * kBuf;
+  static constexpr uint32_t kBars = kMask + kMaskRing * 16;
+  static constexpr uint32_t kEnd = kBars + 256;
+};
+constexpr size_t kSmem = 1024 + Layout::kEnd;
+
+struct TcArgs {
+  Args a;
+  int box;       // tokens per TMA box; 0: plain loads only
+  int tiles;     // row tiles of 256 (at most), all sequences together
+  int splits;
+  int part0;     // first partial of this launch; -1: rows are finished here
+};
+
+// ---- instructions beside those of tc.cuh -----------------------------------
+// K-major or MN-major 128-byte-swizzled operand with explicit strides: for the
+// V tile (tokens x 64-element halves) the fast index is the output column,
+// `lbo` leads from one 64-column half to the next, 1024 bytes from 8 tokens to
+// the next 8.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// D[tmem] (+)= A[tmem] * B[smem], one 128 x 128 x 16 step.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Both score maps in units of log2(e).
+struct ScoreMap {
+  float scale;      // scale * log2(e), or scale / softcap with a cap
+  float cap;        // softcap * log2(e), 0 without a cap
+  float slope;      // slope * log2(e)
+};
+// tanh x = 1 - 2 / (1 + e^(2x)): absolute error of a few 2^-24, which the cap's
+// size multiplies, far below the bf16 weights' rounding
+__device__ __forceinline__ float capped(float x, float cap) {
+  const float e = ex2(x * (2.f * pa::kLog2e));
+  return cap - __fdividef(2.f * cap, 1.f + e);
+}
+
+// The tile's rows, found by every warp for itself.
+template <bool kPrefix>
+__device__ __forceinline__ bool find_tile(const Args& a, int tile, int& b, int64_t& r0, pa::Seq& s) {
+  if constexpr (kPrefix) {
+    b = 0, s = pa::Seq{0, a.T, 0}, r0 = (int64_t)tile * 2 * kTile;
+    return r0 < a.T * a.g;
+  } else {
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      pa::Seq mine{0, 0, 0};
+      if (b0 + lane < a.B) mine = pa::seq_of(a, b0 + lane, false);
+      const int n = (int)((mine.n_new * a.g + 2 * kTile - 1) / (2 * kTile));
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, base + upto > tile);
+      if (m) {
+        const int l = __ffs(m) - 1;
+        b = b0 + l;
+        s = pa::seq_of(a, b, false);
+        const int before = base + __shfl_sync(0xffffffffu, upto - n, l);
+        r0 = (int64_t)(tile - before) * 2 * kTile;
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+  }
+}
+
+// One tile of K or V into `dst` by a whole warp; true when TMA does it (the
+// barrier then completes by bytes, else lane 0 has arrived).  `valid` gets the
+// mask of tokens that were there.
+__device__ __forceinline__ void load_tile(const TcArgs& t, const void* pool, const CUtensorMap* map,
+                                          const int32_t* __restrict__ table, int u0, int n, int j, unsigned char* dst,
+                                          uint64_t* bar, uint4* valid) {
+  const Args& a = t.a;
+  const int lane = threadIdx.x & 31, P = a.pm.page_size;
+  if (t.box > 0 && u0 + kTile <= n) {
+    const int boxes = kTile / t.box;  // at most 16
+    int64_t row = 0;
+    bool ok = true;
+    if (lane < boxes) {
+      row = pa::pool_row(a, table, u0 + lane * t.box, j);
+      ok = row >= 0;
+    }
+    if (__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) {
+        if (valid) *valid = make_uint4(~0u, ~0u, ~0u, ~0u);
+        tc::mbar_expect_tx(bar, kBuf);
+      }
+      __syncwarp();
+      if (lane < boxes) {
+        tc::tma_load_2d(dst + lane * t.box * 128, map, 0, (int)row, bar);
+        tc::tma_load_2d(dst + kHalf + lane * t.box * 128, map, 64, (int)row, bar);
+      }
+      return;
+    }
+  }
+  // plain loads: lane l finds the rows of tokens l, l + 32, l + 64, l + 96
+  int64_t rows[4];
+  uint32_t mask[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int u = u0 + 32 * k + lane;
+    rows[k] = u < n ? pa::pool_row(a, table, u, j) : -1;
+    if (u < n && rows[k] < 0) report(a.status, HKV_ERR_DEVICE_RANGE);
+    mask[k] = __ballot_sync(0xffffffffu, rows[k] >= 0);
+  }
+  if (valid && lane == 0) *valid = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+  const int c = lane & 15;  // 16-byte piece of a row
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    for (int x0 = 0; x0 < 32; x0 += 16) {
+      uint4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t row = __shfl_sync(0xffffffffu, rows[k], x0 + 2 * e + (lane >> 4));
+        v[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (row >= 0) v[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + row * kHeadDim) + c);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int x = 32 * k + x0 + 2 * e + (lane >> 4);
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + x * 128 + (((c & 7) ^ (x & 7)) << 4)) = v[e];
+      }
+    }
+  async_fence();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(bar);
+}
+
+template <bool kPrefix, bool kGeneral>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ TcArgs t) {
+  const Args& a = t.a;
+  constexpr uint32_t kIdescS = tc::idesc_bf16_f32(kTile, kTile);
+  constexpr uint32_t kIdescO = kIdescS | (1u << 16);  // B (V) with the output column as its fast index
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  uint4* valid_s = reinterpret_cast<uint4*>(smem + Layout::kMask);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Layout::kBars);
+  uint64_t* k_full = bars;                    // [kKStages]
+  uint64_t* k_empty = k_full + kKStages;
+  uint64_t* v_full = k_empty + kKStages;      // [kVStages]
+  uint64_t* v_empty = v_full + kVStages;
+  uint64_t* s_full = v_empty + kVStages;      // [slot] S in tensor memory
+  uint64_t* p_full = s_full + 2;              // [slot] P in tensor memory, O rescaled
+  uint64_t* o_done = p_full + 2;              // [slot] O holds the tile
+  uint64_t* idle = o_done + 2;                // [slot] every MMA issued has finished
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(idle + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* range = reinterpret_cast<int*>(tmem_slot + 2);  // [slot][lo, hi]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int j = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv;
+  const int split = rest % t.splits, tile = t.tiles - 1 - rest / t.splits;  // long causal tiles first
+  int b;
+  int64_t r0;
+  pa::Seq seq;
+  if (!find_tile<kPrefix>(a, tile, b, r0, seq)) return;
+  if (threadIdx.x == 0 && r0 == 0 && split == 0 && j == 0 && !kPrefix) pa::seq_of(a, b, true);  // report a cut length
+  const int nrows = (int)min((int64_t)2 * kTile, seq.n_new * a.g - r0);
+  const bool both = nrows > kTile;  // the slots hold different rows and share every tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKStages; ++i) tc::mbar_init(&k_full[i], 1), tc::mbar_init(&k_empty[i], both ? 2 : 1);
+    for (int i = 0; i < kVStages; ++i) tc::mbar_init(&v_full[i], 1), tc::mbar_init(&v_empty[i], both ? 2 : 1);
+    for (int i = 0; i < 2; ++i) {
+      const int rows = both ? min(kTile, nrows - i * kTile) : nrows;
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], (rows + 31) / 32 * 32);  // warps without a row take no part
+      tc::mbar_init(&o_done[i], 1);
+      tc::mbar_init(&idle[i], 1);
+      range[2 * i] = INT32_MAX, range[2 * i + 1] = 0;
+    }
+    *abort = 0;
+    tc::mbar_init_fence();
+  }
+  if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
+  __syncthreads();
+
+  // ---- rows: queries to shared memory, what each row sees ----
+  const int slot = warp >> 2;  // of the softmax warps
+  const int row = both ? threadIdx.x : (threadIdx.x & (kTile - 1));
+  const bool live = warp < 8 && row < nrows;
+  const int64_t tok = (r0 + row) / a.g;
+  const int head = (int)((r0 + row) % a.g);
+  pa::Span sp{0, INT32_MAX, 0};  // rows that are only padding see everything: no masks for their sake
+  if (live) {
+    if constexpr (kPrefix) {
+      const int64_t n = min((int64_t)max(a.n_tok[tok], 0), a.n_max);
+      sp = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
+    } else {
+      sp = pa::span_of(a, seq, b, tok);
+    }
+    if (sp.lo < sp.hi) {
+      atomicMin(&range[2 * slot], sp.lo);
+      atomicMax(&range[2 * slot + 1], sp.hi);
+    }
+  }
+  if (warp < (both ? 8 : 4)) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (seq.first + tok) * a.q_stride + (int64_t)(j * a.g + head) * kHeadDim;
+    unsigned char* dst = smem + Layout::kQ + (row >> 7) * kBuf + (row & 127) * 128;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = v;
+    }
+    async_fence();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int n_all = kPrefix ? (int)a.n_prefix : (int)seq.n;
+  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)b * a.pm.max_pages;
+  // tiles of the CTA, then this split's run of them
+  const int lo = min(range[0], range[2]), hi = max(range[1], range[3]);
+  const int first = lo < hi ? lo / kTile : 0, last = lo < hi ? (hi + kTile - 1) / kTile : 0;
+  const int per = (last - first + t.splits - 1) / t.splits;
+  const int t0 = first + split * per, t1 = min(last, t0 + per);
+
+  // the tiles that slot s works on: whether tile n is one of them
+  auto is_mine = [&](int n, int s) { return both || ((n - t0) & 1) == s; };
+  auto is_seen = [&](int n, int s) { return !both || (n >= range[2 * s] / kTile && n * kTile < range[2 * s + 1]); };
+
+  float m = -INFINITY, l = 0.f;
+  int done = 0;  // tiles that this slot has been through
+  if (warp == 8 || warp == 9) {
+    // ---------------- K and V tiles ----------------
+    const bool is_k = warp == 8;
+    const int stages = is_k ? kKStages : kVStages;
+    uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+    unsigned char* ring = smem + (is_k ? Layout::kK : Layout::kV);
+    const CUtensorMap* map = is_k ? &kmap : &vmap;
+    if (t.box > 0 && lane == 0) tc::tma_prefetch_map(map);
+    int stage = 0, armed = 0;
+    uint32_t phase = 0;
+    for (int n = t0; n < t1; ++n) {
+      const bool ok = tc::mbar_wait(&empty[stage], phase ^ 1u, abort, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      load_tile(t, is_k ? a.K : a.V, map, table, n * kTile, n_all, j, ring + stage * kBuf, &full[stage],
+                is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
+      ++armed;
+      if (++stage == stages) stage = 0, phase ^= 1u;
+    }
+    // on an abort, let every load already issued land before the CTA leaves
+    if (*abort && lane == 0)
+      for (int n = max(0, armed - stages); n < armed; ++n) tc::mbar_drain(&full[n % stages], (n / stages) & 1, a.wait_ns);
+  } else if (warp >= 10) {
+    // ---------------- MMAs ----------------
+    const int s = warp - 10;
+    if (lane == 0) {
+      const uint32_t s_tmem = tmem + s * 256, o_tmem = s_tmem + kTile;
+      const uint32_t q_addr = tc::smem_u32(smem + Layout::kQ + (both ? s : 0) * kBuf);
+      for (int n = t0; n < t1; ++n) {
+        if (!is_mine(n, s)) continue;
+        const int c = n - t0, ks = c % kKStages, vs = c % kVStages;
+        const bool seen = is_seen(n, s);
+        if (!tc::mbar_wait(&k_full[ks], (c / kKStages) & 1, abort, a.wait_ns)) break;
+        if (!seen) {
+          tc::mbar_arrive(&k_empty[ks]);
+          if (!tc::mbar_wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns)) break;
+          tc::mbar_arrive(&v_empty[vs]);
+          continue;
+        }
+        tc::fence_after_sync();
+        const uint32_t k_addr = tc::smem_u32(smem + Layout::kK + ks * kBuf);
+        // S of this tile overwrites the last tile's P: MMAs of one thread run in order
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16(s_tmem, tc::sw128_desc(q_addr + (kk >> 2) * kHalf + (kk & 3) * 32),
+                       tc::sw128_desc(k_addr + (kk >> 2) * kHalf + (kk & 3) * 32), kIdescS, kk != 0);
+        tc::mma_commit(&s_full[s]);
+        tc::mma_commit(&k_empty[ks]);
+        if (!tc::mbar_wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns)) break;
+        if (!tc::mbar_wait(&p_full[s], done & 1, abort, a.wait_ns)) break;
+        tc::fence_after_sync();
+        const uint32_t v_addr = tc::smem_u32(smem + Layout::kV + vs * kBuf);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(o_tmem, s_tmem + kk * 8, sw128_desc_mn(v_addr + kk * 16 * 128, kHalf), kIdescO, (done | kk) != 0);
+        tc::mma_commit(&v_empty[vs]);
+        tc::mma_commit(&o_done[s]);
+        ++done;
+      }
+      tc::mma_commit(&idle[s]);
+      tc::mbar_drain(&idle[s], 0, a.wait_ns);
+    }
+  } else if (both ? warp * 32 < nrows : (warp & 3) * 32 < nrows) {
+    // ---------------- softmax: one row per thread ----------------
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256;
+    const uint32_t s_tmem = lane_base, o_tmem = lane_base + kTile;
+    ScoreMap sm;
+    sm.scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
+    sm.cap = a.softcap * pa::kLog2e;
+    sm.slope = a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
+    for (int n = t0; n < t1; ++n) {
+      if (!is_mine(n, slot) || !is_seen(n, slot)) continue;
+      const bool ok = tc::mbar_wait(&s_full[slot], done & 1, abort, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc::fence_after_sync();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tc::tmem_ld32(s_tmem + 32 * k, v[k]);
+      tc::tmem_wait_ld();
+      const int u0 = n * kTile;
+      if constexpr (kGeneral) {
+        const float d0 = (float)(sp.pos - u0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float z = __uint_as_float(v[k][i]) * sm.scale;
+            if (sm.cap > 0.f) z = capped(z, sm.cap);
+            v[k][i] = __float_as_uint(fmaf(-sm.slope, fabsf(d0 - (float)(32 * k + i)), z));
+          }
+      }
+      const uint4 there = valid_s[(n - t0) % kMaskRing];
+      const bool whole = sp.lo <= u0 && sp.hi >= u0 + kTile && (there.x & there.y & there.z & there.w) == ~0u;
+      if (__any_sync(0xffffffffu, !whole)) {
+        const uint32_t w[4] = {there.x, there.y, there.z, there.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int u = u0 + 32 * k + i;
+            if (u < sp.lo || u >= sp.hi || !(w[k] >> i & 1u)) v[k][i] = 0xff800000u;  // -inf
+          }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[k][i]));
+      const float c = kGeneral ? 1.f : sm.scale;  // positive: the largest product is the largest score
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const bool grown = top > m + kGrowth || (m == -INFINITY && top > -INFINITY);
+      if (__any_sync(0xffffffffu, grown)) {
+        float f = 1.f;
+        if (grown) f = ex2(m - top), l *= f, m = top;  // m = -inf: 0
+        if (done > 0) {
+          const bool ok2 = tc::mbar_wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
+          if (!__all_sync(0xffffffffu, ok2)) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_tmem + 32 * k, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(o_tmem + 32 * k, o);
+          }
+        }
+      }
+      const float off = m == -INFINITY ? 0.f : m;
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x = ex2(fmaf(__uint_as_float(v[k][2 * i]), c, -off));
+          const float y = ex2(fmaf(__uint_as_float(v[k][2 * i + 1]), c, -off));
+          sum[0] += x, sum[1] += y;
+          p[i] = pack_bf16(x, y);
+        }
+        tmem_st16(s_tmem + 16 * k, p);
+      }
+      l += sum[0] + sum[1];
+      tmem_wait_st();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&p_full[slot]);
+      ++done;
+    }
+    if (done > 0) {
+      const bool ok = tc::mbar_wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
+      __all_sync(0xffffffffu, ok);
+      tc::fence_after_sync();
+    }
+  }
+
+  // ---- results ----
+  const uint32_t o_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256 + kTile;
+  float scale1 = 0.f;  // weight of the other slot's O, when it has the same rows
+  float* const other = reinterpret_cast<float*>(smem + Layout::kK);  // [128 columns][128 rows], then m, l
+  if (!both) {
+    tc::fence_before_sync();
+    __syncthreads();  // every MMA has finished: the tiles' memory is free
+    tc::fence_after_sync();
+    if (warp >= 4 && warp < 8 && (warp & 3) * 32 < nrows) {
+      other[kTile * kTile + row] = m, other[kTile * kTile + kTile + row] = l;
+      if (done > 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[32];
+          tc::tmem_ld32(o_tmem + 32 * k, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) other[(32 * k + i) * kTile + row] = __uint_as_float(o[i]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const bool writes = both ? warp < 8 && warp * 32 < nrows : warp < 4 && warp * 32 < nrows;
+  if (writes && !*abort) {
+    float scale0 = 1.f;
+    if (!both) {
+      const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
+      const float top = fmaxf(m, m1);
+      scale0 = m == -INFINITY ? 0.f : ex2(m - top);
+      scale1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+      l = l * scale0 + l1 * scale1, m = top;
+    }
+    const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
+    const bool partial = t.part0 >= 0;
+    const float inv = partial ? 1.f : l > 0.f ? 1.f / l : 0.f;
+    const int64_t part_row = partial ? (t.part0 + split) * a.T * a.Hq + out_row : 0;
+    if (live && partial) a.part_ml[part_row] = make_float2(m, l);
+    if (live && !partial && a.lse) a.lse[out_row] = l > 0.f ? (m + log2f(l)) * pa::kLn2 : -INFINITY;
+    const bool none = m == -INFINITY;  // nothing seen: O was never written, or is zero
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[32];
+      tc::tmem_ld32(o_tmem + 32 * k, o);
+      tc::tmem_wait_ld();
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        x[i] = scale0 > 0.f ? __uint_as_float(o[i]) * scale0 : 0.f;
+        if (!both && scale1 > 0.f) x[i] = fmaf(other[(32 * k + i) * kTile + row], scale1, x[i]);
+        x[i] = none ? 0.f : x[i] * inv;
+      }
+      if (live && partial) {
+        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      } else if (live) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kHeadDim + 32 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                              pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort) report(a.status, HKV_ERR_TIMEOUT);
+  if (warp == 10) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_free(tmem, 512);
+  }
+}
+
+// Joins the splits of a prompt's rows: one warp per row, four columns per lane.
+__global__ void __launch_bounds__(256)
+join_parts_kernel(const __grid_constant__ Args a, int parts) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= a.T * a.Hq) return;
+  const int64_t t = row / a.Hq, n_rows = a.T * a.Hq;
+  const int b = pa::find_seq(a.cu, a.B, t);
+  const pa::Seq s = pa::seq_of(a, b, false);
+  if (t < s.first || t >= s.first + s.n_new) return;  // behind the last sequence
+  float M = -INFINITY;
+  for (int p = 0; p < parts; ++p) M = fmaxf(M, a.part_ml[p * n_rows + row].x);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < parts; ++p) {
+    const float2 ml = a.part_ml[p * n_rows + row];
+    if (ml.x == -INFINITY) continue;
+    const float w = exp2f(ml.x - M);
+    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (p * n_rows + row) * kHeadDim + lane * 4);
+    L = fmaf(w, ml.y, L);
+    o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHeadDim + lane * 4) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (lane == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
+
+// The pool as rows of 128 bf16, read in boxes of `box` rows x 64 columns.
+int pool_map(CUtensorMap* map, const void* pool, int64_t rows, int box) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return fail(HKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kHeadDim * 2};
+  const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, ones[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, boxes, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? HKV_OK : fail(HKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+}
+
+}  // namespace
+
+// Row tiles of all sequences together, at most: a sequence's last tile may be
+// partly filled.
+int64_t tc_tiles(const PagedAttend& p, bool prefix) {
+  const int64_t rows = p.T * (p.Hq / p.Hkv);
+  return prefix ? ceil_div(rows, 2 * kTile) : rows / (2 * kTile) + (p.B < p.T ? p.B : p.T);
+}
+
+// One wave of CTAs where the rows alone leave SMs idle, each with at least
+// four tiles of positions (a CTA's prologue and the joining of parts cost
+// about as much as two tiles).
+int tc_splits(const PagedAttend& p, bool prefix) {
+  const int64_t ctas = tc_tiles(p, prefix) * p.Hkv, sms = sm_count();
+  const int64_t most = ceil_div(prefix ? p.n_prefix : p.n_max, 4 * kTile);
+  int64_t s = sms / (ctas < 1 ? 1 : ctas);
+  s = s < most ? s : most;
+  return (int)(s < 1 ? 1 : s);
+}
+
+int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int splits, int part0, cudaStream_t st) {
+  TcArgs t{a, 0, (int)tc_tiles(p, prefix), splits, part0};
+  // the largest power of two that divides the page: a box never leaves its
+  // page, and whole swizzle groups of 8 rows keep the tile's layout
+  int box = p.pm.page_size & -p.pm.page_size;
+  box = box < kTile ? box : kTile;
+  const int64_t rows = p.pm.num_pages * p.Hkv * p.pm.page_size;
+  alignas(64) CUtensorMap kmap{}, vmap{};
+  if (box >= 8 && rows <= INT32_MAX) {
+    int rc = pool_map(&kmap, p.K_pool, rows, box);
+    if (rc == HKV_OK) rc = pool_map(&vmap, p.V_pool, rows, box);
+    if (rc != HKV_OK) return rc;
+    t.box = box;
+  }
+  const bool general = a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f);
+  auto kernel = prefix ? (general ? attend_tc_kernel<true, true> : attend_tc_kernel<true, false>)
+                       : (general ? attend_tc_kernel<false, true> : attend_tc_kernel<false, false>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return cuda_check(e, "attention smem attribute");
+  const int64_t grid = (int64_t)t.tiles * splits * p.Hkv;
+  if (grid > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "too many row tiles (%lld)", (long long)grid);
+  kernel<<<(unsigned)grid, kThreads, kSmem, st>>>(kmap, vmap, t);
+  int rc = cuda_check(cudaGetLastError(), "attention launch");
+  if (rc != HKV_OK || prefix || part0 < 0) return rc;
+  join_parts_kernel<<<(unsigned)ceil_div(a.T * a.Hq, 8), 256, 0, st>>>(a, splits);
+  return cuda_check(cudaGetLastError(), "attention join launch");
+}
+
+}  // namespace hkv

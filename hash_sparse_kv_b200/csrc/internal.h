@@ -151,7 +151,8 @@ struct PagedAttend {
   int64_t q_stride;
   const void *K_pool, *V_pool;
   PageMap pm;
-  const int32_t* cu_q;   // null: one token a sequence
+  bool cu_q_rows;        // rows per sequence go by cu_q (prompts); else one token a sequence
+  const int32_t* cu_q;
   const int32_t* n_tok;
   int64_t n_max;
   const int32_t* prefix_table;
