@@ -473,6 +473,9 @@ int hkv_append_paged(const hkv_hash* hash, int dtype, const hkv_rope* rope, int 
   return launch_append_paged(p, pm, ws, static_cast<cudaStream_t>(stream));
 }
 
+// Positions are 32-bit in the kernels, a tile of them past the last included.
+constexpr int64_t kMaxAttendTokens = INT32_MAX - 255;
+
 // What both dense attention calls check; `p` is filled as far as they share it.
 static int check_attend(int B, int64_t T, int Hq, int Hkv, int dtype, float scale, const hkv_score* score,
                         PagedAttend& p) {
@@ -499,13 +502,15 @@ static int check_attend_pools(const PagedAttend& p, const void* ws) {
   if (!p.K_pool || !p.V_pool || !p.out || !p.n_tok) return fail(HKV_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(p.K_pool, 16) || !aligned(p.V_pool, 16) || !aligned(p.out, 16))
     return fail(HKV_ERR_INVALID_ARG, "K_pool, V_pool and out must be 16-byte aligned");
+  if (p.pm.num_pages > INT32_MAX || p.pm.num_pages * p.pm.page_size > INT32_MAX / p.Hkv)
+    return fail(HKV_ERR_UNSUPPORTED, "a pool of more than 2^31 - 1 rows");
   if (!aligned(ws, 256)) return fail(HKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   return HKV_OK;
 }
 
 static int check_prefill(int64_t T, int max_q, int64_t n_max, PagedAttend& p) {
   if (max_q < 0 || n_max < 0) return fail(HKV_ERR_INVALID_ARG, "max_q %d n_tokens_max %lld", max_q, (long long)n_max);
-  if (n_max > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "n_tokens_max %lld > 2^31-1", (long long)n_max);
+  if (n_max > kMaxAttendTokens) return fail(HKV_ERR_UNSUPPORTED, "n_tokens_max %lld > 2^31 - 256", (long long)n_max);
   p.cu_q_rows = true;
   p.max_q = max_q < T ? max_q : (int)T;
   p.n_max = n_max;
@@ -541,8 +546,8 @@ int hkv_prefill_attend_paged(int B, int64_t T, int Hq, int Hkv, int dtype, const
 static int check_shared(int64_t n_prefix, int64_t n_own_max, PagedAttend& p) {
   if (n_prefix < 0 || n_own_max < 0)
     return fail(HKV_ERR_INVALID_ARG, "n_prefix %lld n_own_max %lld", (long long)n_prefix, (long long)n_own_max);
-  if (n_prefix > INT32_MAX || n_own_max > INT32_MAX || n_prefix + n_own_max > INT32_MAX)
-    return fail(HKV_ERR_UNSUPPORTED, "n_prefix + n_own_max > 2^31-1");
+  if (n_prefix > kMaxAttendTokens || n_own_max > kMaxAttendTokens || n_prefix + n_own_max > kMaxAttendTokens)
+    return fail(HKV_ERR_UNSUPPORTED, "n_prefix + n_own_max > 2^31 - 256");
   p.max_q = 1, p.n_max = n_own_max, p.n_prefix = n_prefix;
   return HKV_OK;
 }

@@ -20,9 +20,13 @@ using pa::Args;
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
 constexpr int kTile = 32;
+constexpr int kMaxParts = 224;  // parts that a row is joined from, at most
 
-__device__ __forceinline__ void put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 
 // Which rows a block has and which positions of which table they see.
 struct Item {
@@ -65,24 +69,23 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Item& it, int r)
   return (it.row0 + r / a.g) * a.Hq + it.j * a.g + r % a.g;
 }
 
-// The block's partial result: `m_s`, `l_s` of its rows (shared memory) and
-// acc[k], the weighted values of row (tid / 128) * 8 + k, column tid % 128.
+// The block's result: maximum, sum and weighted values of its rows, in shared
+// memory (o_s [kRows][kHeadDim], m_s and l_s [kRows]).  `w_s` is shared memory for
+// kRows * parts weights.  Every thread of the block comes here after a barrier.
 template <typename T, bool kPrefix>
-__device__ void finish(const Args& a, const Item& it, const float (&acc)[8], const float* m_s, const float* l_s,
+__device__ void finish(const Args& a, const Item& it, const float* o_s, const float* m_s, const float* l_s, float* w_s,
                        int* last_s) {
-  const int tid = threadIdx.x, col = tid % kHeadDim, r0 = tid / kHeadDim * 8;
+  constexpr int Q = kHeadDim / 4;  // float4 pieces of a row
+  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int64_t n_rows = a.T * a.Hq;
-  const int parts = a.prefix_parts + a.own_parts;
   const int mine = kPrefix ? blockIdx.z : a.prefix_parts + blockIdx.z;
   const bool alone = !kPrefix && a.own_parts == 1;  // this block's partial need not go through memory
   if (!alone) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (r0 + k < it.nrows) {
-        const int64_t row = mine * n_rows + out_row(a, it, r0 + k);
-        a.part_o[row * kHeadDim + col] = acc[k];
-        if (col == 0) a.part_ml[row] = make_float2(m_s[r0 + k], l_s[r0 + k]);
-      }
+    for (int i = tid; i < it.nrows * Q; i += nthr) {
+      const int64_t row = mine * n_rows + out_row(a, it, i / Q);
+      reinterpret_cast<float4*>(a.part_o)[row * Q + i % Q] = reinterpret_cast<const float4*>(o_s)[i];
+      if (i % Q == 0) a.part_ml[row] = make_float2(m_s[i / Q], l_s[i / Q]);
+    }
     if constexpr (kPrefix) return;
     __threadfence();
     __syncthreads();
@@ -95,29 +98,51 @@ __device__ void finish(const Args& a, const Item& it, const float (&acc)[8], con
     if (!*last_s) return;
     __threadfence();
   }
-  const int from_memory = alone ? a.prefix_parts : parts;
+  const int parts = alone ? a.prefix_parts : a.prefix_parts + a.own_parts;
+  // a warp per row: the parts' weights, this block's own (if it is not among
+  // them) last, and the log-sum-exp
+  for (int r = warp; r < it.nrows; r += nthr / 32) {
+    const int64_t row = out_row(a, it, r);
+    float M = alone ? m_s[r] : -INFINITY;
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(&a.part_ml[p * n_rows + row].x));
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (r0 + k >= it.nrows) continue;
-    const int64_t row = out_row(a, it, r0 + k);
-    float M = alone ? m_s[r0 + k] : -INFINITY;
-    for (int p = 0; p < from_memory; ++p) M = fmaxf(M, __ldcg(&a.part_ml[p * n_rows + row].x));
-    float L = 0.f, o = 0.f;
-    if (M != -INFINITY) {
-      if (alone) {
-        const float w = exp2f(m_s[r0 + k] - M);
-        L = w * l_s[r0 + k], o = w * acc[k];
-      }
-      for (int p = 0; p < from_memory; ++p) {
-        const float2 ml = __ldcg(&a.part_ml[p * n_rows + row]);
-        if (ml.x == -INFINITY) continue;  // an empty part's values need not be written
-        const float w = exp2f(ml.x - M);
-        L = fmaf(w, ml.y, L);
-        o = fmaf(w, __ldcg(&a.part_o[(p * n_rows + row) * kHeadDim + col]), o);
-      }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    for (int p = lane; p < parts; p += 32) {
+      const float2 ml = __ldcg(&a.part_ml[p * n_rows + row]);
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      w_s[r * (parts + 1) + p] = w;
+      L = fmaf(w, ml.y, L);
     }
-    put(static_cast<T*>(a.out) + row * kHeadDim + col, L > 0.f ? o / L : 0.f);
-    if (col == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float own = alone && m_s[r] != -INFINITY ? exp2f(m_s[r] - M) : 0.f;
+    if (alone) L = fmaf(own, l_s[r], L);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    __syncwarp();
+    for (int p = lane; p < parts; p += 32) w_s[r * (parts + 1) + p] *= inv;
+    if (lane == 0) {
+      w_s[r * (parts + 1) + parts] = own * inv;
+      if (a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < it.nrows * Q; i += nthr) {
+    const int r = i / Q;
+    const int64_t row = out_row(a, it, r);
+    const float* w = w_s + r * (parts + 1);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (w[parts] > 0.f) {
+      const float4 x = reinterpret_cast<const float4*>(o_s)[i];
+      o = make_float4(w[parts] * x.x, w[parts] * x.y, w[parts] * x.z, w[parts] * x.w);
+    }
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) {
+      if (w[p] == 0.f) continue;  // an empty part's values need not have been written
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (p * n_rows + row) * Q + i % Q);
+      o.x = fmaf(w[p], x.x, o.x), o.y = fmaf(w[p], x.y, o.y), o.z = fmaf(w[p], x.z, o.z), o.w = fmaf(w[p], x.w, o.w);
+    }
+    put4(static_cast<T*>(a.out) + row * kHeadDim + i % Q * 4, o);
   }
 }
 
@@ -125,9 +150,9 @@ template <typename T, bool kPrefix>
 __global__ void __launch_bounds__(kThreads)
 rows_simt_kernel(const __grid_constant__ Args a) {
   constexpr int D = kHeadDim, KP = D + 1;
-  __shared__ float q_s[kRows][D];
-  __shared__ float k_s[kTile][KP];
-  __shared__ float v_s[kTile][D];
+  __shared__ __align__(16) float q_s[kRows][D];  // the block's result in the end
+  __shared__ __align__(16) float k_s[kTile][KP];
+  __shared__ __align__(16) float v_s[kTile][D];  // the joined parts' weights in the end
   __shared__ float p_s[kRows][kTile];
   __shared__ float m_s[kRows], l_s[kRows], f_s[kRows];
   __shared__ int64_t row_s[kTile];
@@ -224,7 +249,256 @@ rows_simt_kernel(const __grid_constant__ Args a) {
     }
   }
   __syncthreads();
-  finish<T, kPrefix>(a, it, acc, m_s, l_s, &last_s);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) q_s[ar0 + k][col] = acc[k];
+  __syncthreads();
+  static_assert(kRows * (kMaxParts + 1) <= kTile * D, "weights must fit v_s");
+  finish<T, kPrefix>(a, it, q_s[0], m_s, l_s, v_s[0], &last_s);
+}
+
+// ---- bf16: the same on the tensor cores of one warp --------------------------
+// Each of four warps takes every fourth step of 16 tokens with a ring of its
+// own (cp.async, three steps of 8 KB: 192 KB in flight on an SM with two
+// blocks), so nothing but the end of the block makes warps wait for each
+// other.  Scores and products are mma.sync m16n8k16 with the 16 rows as M: the
+// block is bound by reading K and V, and a 128-row tcgen05 tile would be seven
+// eighths padding.  P is rounded to bf16 for the product, sums stay fp32.
+constexpr int kMmaThreads = 128;
+constexpr int kMmaWarps = kMmaThreads / 32;
+constexpr int kStep = 16;                    // tokens
+constexpr int kStages = 3;
+constexpr int kStepBytes = kStep * 256;      // of K, and again of V
+constexpr int kQPitch = kHeadDim + 8;
+constexpr size_t kMmaSmem = (size_t)kMmaWarps * kStages * 2 * kStepBytes;
+
+__device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <bool kGeneral>
+__global__ void __launch_bounds__(kMmaThreads, 2)
+rows_mma_kernel(const __grid_constant__ Args a) {
+  constexpr int D = kHeadDim;
+  extern __shared__ __align__(128) unsigned char ring[];  // [warp][stage][K step, V step]; the parts in the end
+  __shared__ __align__(16) __nv_bfloat16 q_s[kRows][kQPitch];
+  __shared__ float m_s[kMmaWarps][kRows], l_s[kMmaWarps][kRows];
+  __shared__ int span_s[2], last_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Item it;
+  if (!item_of<false>(a, it)) return;
+  for (int i = tid; i < kRows * (D / 8); i += kMmaThreads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < it.nrows)
+      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + r / a.g) * a.q_stride +
+                                               (int64_t)(it.j * a.g + r % a.g) * D) + c);
+    *reinterpret_cast<uint4*>(&q_s[r][c * 8]) = v;
+  }
+  // this thread's two rows of every fragment; padding rows see everything
+  pa::Span sp[2];
+  float slope[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = lane / 4 + 8 * h;
+    sp[h] = r < it.nrows ? row_span<false>(a, it, r) : pa::Span{0, INT32_MAX, 0};
+    slope[h] = kGeneral && a.slopes && r < it.nrows ? a.slopes[it.j * a.g + r % a.g] * pa::kLog2e : 0.f;
+  }
+  if (warp == 0) {
+    int lo = INT32_MAX, hi = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (lane / 4 + 8 * h < it.nrows && sp[h].lo < sp[h].hi) lo = min(lo, sp[h].lo), hi = max(hi, sp[h].hi);
+    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) span_s[0] = min(lo, hi), span_s[1] = hi;
+  }
+  __syncthreads();
+  const int lo = span_s[0], hi = span_s[1];
+  // this block's run of steps, aligned to steps of the sequence
+  const int s0 = lo / kStep, s1 = (hi + kStep - 1) / kStep, per = (s1 - s0 + gridDim.z - 1) / gridDim.z;
+  const int first = s0 + (int)blockIdx.z * per, last = hi > lo ? min(s1, first + per) : first;
+  uint32_t qf[8][4];
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) ldsm4(qf[kk], sm32(&q_s[lane % 16][kk * 16 + lane / 16 * 8]));
+
+  const int32_t* __restrict__ table = a.pm.table + (int64_t)it.b * a.pm.max_pages;
+  const uint32_t P = a.pm.page_size, pages = (uint32_t)a.pm.num_pages;
+  const uint32_t my_ring = sm32(ring) + warp * kStages * 2 * kStepBytes;
+  const __nv_bfloat16 *Kp = static_cast<const __nv_bfloat16*>(a.K), *Vp = static_cast<const __nv_bfloat16*>(a.V);
+  // lane l (and l + 16) looks up token l of a step, one step before its loads
+  auto page_of = [&](int step) -> int {
+    const uint32_t u = (uint32_t)step * kStep + (lane & 15);
+    return step < last && (int)u < hi ? table[u / P] : -1;
+  };
+  uint32_t there[kStages];  // tokens of each stage that have a place in the pool
+  auto issue = [&](int step, int page, int stage) -> uint32_t {
+    const uint32_t u = (uint32_t)step * kStep + (lane & 15);
+    const bool in = step < last && (int)u < hi;
+    const bool ok = in && (uint32_t)page < pages;
+    if (in && !ok && lane < 16) report(a.status, HKV_ERR_DEVICE_RANGE);
+    const uint32_t row = ok ? ((uint32_t)page * a.Hkv + it.j) * P + u % P : 0xffffffffu;
+    if (step < last) {
+      const uint32_t base = my_ring + stage * 2 * kStepBytes;
+      const int c = lane & 15;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int x = 2 * i + (lane >> 4);
+        const uint32_t rx = __shfl_sync(0xffffffffu, row, x);
+        const uint32_t dst = base + x * 256 + ((c ^ (x & 7)) << 4);
+        const int64_t off = rx == 0xffffffffu ? 0 : (int64_t)rx * D + c * 8;
+        const int bytes = rx == 0xffffffffu ? 0 : 16;
+        cp16(dst, Kp + off, bytes);
+        cp16(dst + kStepBytes, Vp + off, bytes);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return __ballot_sync(0xffffffffu, ok) & 0xffffu;
+  };
+
+  float acc[16][4] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
+  const float cap = a.softcap * pa::kLog2e;
+  int page = page_of(first + warp);
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    const int step = first + warp + s * kMmaWarps, next = page_of(step + kMmaWarps);
+    there[s] = issue(step, page, s);
+    page = next;
+  }
+  for (int step0 = first + warp; step0 < last; step0 += kStages * kMmaWarps) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      const int step = step0 + s * kMmaWarps;
+      if (step >= last) break;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const uint32_t kb = my_ring + s * 2 * kStepBytes, vb = kb + kStepBytes;
+      float z[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        // tokens 0-7 and 8-15 of the step, elements kk * 16 + 0-7 and 8-15
+        uint32_t b[4];
+        const int x = (lane & 7) + (lane >> 4) * 8, ch = kk * 2 + ((lane >> 3) & 1);
+        ldsm4(b, kb + x * 256 + ((ch ^ (x & 7)) << 4));
+        mma16816(z[0], qf[kk], b[0], b[1]);
+        mma16816(z[1], qf[kk], b[2], b[3]);
+      }
+      const int u0 = step * kStep + (lane & 3) * 2;  // this thread's tokens: u0, u0 + 1, u0 + 8, u0 + 9
+      float top[2] = {-INFINITY, -INFINITY};
+      const bool whole = there[s] == 0xffffu && sp[0].lo <= step * kStep && sp[1].lo <= step * kStep &&
+                         sp[0].hi >= (step + 1) * kStep && sp[1].hi >= (step + 1) * kStep;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = e >> 1, u = u0 + n * 8 + (e & 1);
+          float x = z[n][e] * zs;
+          if (kGeneral) {
+            if (cap > 0.f) x = pa::capped(x, cap);
+            x = fmaf(-slope[h], fabsf((float)(sp[h].pos - u)), x);
+          }
+          if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there[s] >> (u & 15) & 1u))) x = -INFINITY;
+          z[n][e] = x;
+          top[h] = fmaxf(top[h], x);
+        }
+      bool grown = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        grown |= top[h] > m[h] + 8.f || (m[h] == -INFINITY && top[h] > -INFINITY);
+      }
+      if (__any_sync(0xffffffffu, grown)) {  // rare after the first steps
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(m[h], top[h]), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          m[h] = mn, l[h] *= f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[i][2 * h] *= f, acc[i][2 * h + 1] *= f;
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int h = e >> 1;
+          z[n][e] = pa::ex2(z[n][e] - (m[h] == -INFINITY ? 0.f : m[h]));
+          l[h] += z[n][e];
+        }
+      const uint32_t pf[4] = {pack2(z[0][0], z[0][1]), pack2(z[0][2], z[0][3]), pack2(z[1][0], z[1][1]),
+                              pack2(z[1][2], z[1][3])};
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t b[4];
+        const int x = lane & 15, ch = d * 2 + (lane >> 4);
+        ldsm4t(b, vb + x * 256 + ((ch ^ (x & 7)) << 4));
+        mma16816(acc[2 * d], pf, b[0], b[1]);
+        mma16816(acc[2 * d + 1], pf, b[2], b[3]);
+      }
+      __syncwarp();
+      const int ahead = step + kStages * kMmaWarps, next = page_of(ahead + kMmaWarps);
+      there[s] = issue(ahead, page, s);
+      page = next;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if ((lane & 3) == 0) m_s[warp][lane / 4 + 8 * h] = m[h], l_s[warp][lane / 4 + 8 * h] = l[h];
+  }
+  __syncthreads();  // every warp's loads have landed and been used: the ring is free
+  // the four warps' results join in shared memory
+  float* o_w = reinterpret_cast<float*>(ring);  // [warp][row][column]
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2*>(&o_w[(warp * kRows + lane / 4 + 8 * h) * D + i * 8 + (lane & 3) * 2]) =
+          make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+  __syncthreads();
+  __shared__ float mm[kRows], ll[kRows], fw[kMmaWarps][kRows];
+  if (tid < kRows) {
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, m_s[w][tid]);
+#pragma unroll
+    for (int w = 0; w < kMmaWarps; ++w) {
+      fw[w][tid] = m_s[w][tid] == -INFINITY ? 0.f : exp2f(m_s[w][tid] - M);
+      L = fmaf(fw[w][tid], l_s[w][tid], L);
+    }
+    mm[tid] = M, ll[tid] = L;
+  }
+  __syncthreads();
+  for (int i = tid; i < it.nrows * D; i += kMmaThreads) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMmaWarps; ++w) x = fmaf(fw[w][i / D], o_w[w * kRows * D + i], x);
+    o_w[i] = x;
+  }
+  __syncthreads();
+  static_assert(kRows * (kMaxParts + 1) * sizeof(float) + kMmaWarps * kRows * D * sizeof(float) <= kMmaSmem, "weights");
+  finish<__nv_bfloat16, false>(a, it, o_w, mm, ll, o_w + kMmaWarps * kRows * D, &last_s);
 }
 
 // Splits that fill the GPU about twice over, each with at least four tiles.
@@ -277,13 +551,22 @@ int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
     const int rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
     if (rc != HKV_OK) return rc;
   } else if (pl.prefix_parts > 0) {
-    const dim3 grid((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts);
-    rows_simt_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
-    const int rc = cuda_check(cudaGetLastError(), "prefix attention launch");
-    if (rc != HKV_OK) return rc;
+    if constexpr (sizeof(T) == 4) {
+      const dim3 grid((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts);
+      rows_simt_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
+      const int rc = cuda_check(cudaGetLastError(), "prefix attention launch");
+      if (rc != HKV_OK) return rc;
+    }
   }
   const dim3 grid((unsigned)pl.own_items, p.Hkv, pl.own_parts);
-  rows_simt_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+  if constexpr (sizeof(T) == 2) {
+    auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmaSmem);
+    if (e != cudaSuccess) return cuda_check(e, "paged attention smem attribute");
+    kernel<<<grid, kMmaThreads, kMmaSmem, st>>>(a);
+  } else {
+    rows_simt_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+  }
   return cuda_check(cudaGetLastError(), "paged attention launch");
 }
 

@@ -102,6 +102,18 @@ __device__ __forceinline__ int64_t pool_row(const Args& a, const int32_t* __rest
   return (page * a.Hkv + j) * a.pm.page_size + u % a.pm.page_size;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// tanh x = 1 - 2 / (1 + e^(2x)): absolute error of a few 2^-24, which the cap's
+// size multiplies, far below the bf16 weights' rounding
+__device__ __forceinline__ float capped(float x, float cap) {
+  const float e = ex2(x * (2.f * kLog2e));
+  return cap - __fdividef(2.f * cap, 1.f + e);
+}
+
 // Sequence of row t: the largest b in [0, B) with cu[b] <= t, found by the
 // whole warp, 32 candidates a round.
 __device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int B, int64_t t) {

@@ -96,11 +96,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -113,13 +108,6 @@ struct ScoreMap {
   float cap;        // softcap * log2(e), 0 without a cap
   float slope;      // slope * log2(e)
 };
-// tanh x = 1 - 2 / (1 + e^(2x)): absolute error of a few 2^-24, which the cap's
-// size multiplies, far below the bf16 weights' rounding
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float e = ex2(x * (2.f * pa::kLog2e));
-  return cap - __fdividef(2.f * cap, 1.f + e);
-}
-
 // The tile's rows, found by every warp for itself.
 template <bool kPrefix>
 __device__ __forceinline__ bool find_tile(const Args& a, int tile, int& b, int64_t& r0, pa::Seq& s) {
@@ -400,7 +388,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float z = __uint_as_float(v[k][i]) * sm.scale;
-            if (sm.cap > 0.f) z = capped(z, sm.cap);
+            if (sm.cap > 0.f) z = pa::capped(z, sm.cap);
             v[k][i] = __float_as_uint(fmaf(-sm.slope, fabsf(d0 - (float)(32 * k + i)), z));
           }
       }
@@ -426,7 +414,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const bool grown = top > m + kGrowth || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xffffffffu, grown)) {
         float f = 1.f;
-        if (grown) f = ex2(m - top), l *= f, m = top;  // m = -inf: 0
+        if (grown) f = pa::ex2(m - top), l *= f, m = top;  // m = -inf: 0
         if (done > 0) {
           const bool ok2 = tc::mbar_wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
           if (!__all_sync(0xffffffffu, ok2)) break;
@@ -449,8 +437,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = ex2(fmaf(__uint_as_float(v[k][2 * i]), c, -off));
-          const float y = ex2(fmaf(__uint_as_float(v[k][2 * i + 1]), c, -off));
+          const float x = pa::ex2(fmaf(__uint_as_float(v[k][2 * i]), c, -off));
+          const float y = pa::ex2(fmaf(__uint_as_float(v[k][2 * i + 1]), c, -off));
           sum[0] += x, sum[1] += y;
           p[i] = pack_bf16(x, y);
         }
@@ -498,8 +486,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (!both) {
       const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
       const float top = fmaxf(m, m1);
-      scale0 = m == -INFINITY ? 0.f : ex2(m - top);
-      scale1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+      scale0 = m == -INFINITY ? 0.f : pa::ex2(m - top);
+      scale1 = m1 == -INFINITY ? 0.f : pa::ex2(m1 - top);
       l = l * scale0 + l1 * scale1, m = top;
     }
     const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
