@@ -108,6 +108,9 @@ struct ScoreMap {
   float cap;        // softcap * log2(e), 0 without a cap
   float slope;      // slope * log2(e)
 };
+// Barrier of the two softmax warpgroups.
+__device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
 // The tile's rows, found by every warp for itself.
 template <bool kPrefix>
 __device__ __forceinline__ bool find_tile(const Args& a, int tile, int& b, int64_t& r0, pa::Seq& s) {
@@ -300,41 +303,42 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   auto is_mine = [&](int n, int s) { return both || ((n - t0) & 1) == s; };
   auto is_seen = [&](int n, int s) { return !both || (n >= range[2 * s] / kTile && n * kTile < range[2 * s + 1]); };
 
-  float m = -INFINITY, l = 0.f;
-  int done = 0;  // tiles that this slot has been through
-  if (warp == 8 || warp == 9) {
-    // ---------------- K and V tiles ----------------
-    const bool is_k = warp == 8;
-    const int stages = is_k ? kKStages : kVStages;
-    uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
-    unsigned char* ring = smem + (is_k ? Layout::kK : Layout::kV);
-    const CUtensorMap* map = is_k ? &kmap : &vmap;
-    if (t.box > 0 && lane == 0) tc::tma_prefetch_map(map);
-    int stage = 0, armed = 0;
-    uint32_t phase = 0;
-    for (int n = t0; n < t1; ++n) {
-      const bool ok = tc::mbar_wait(&empty[stage], phase ^ 1u, abort, a.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      load_tile(t, is_k ? a.K : a.V, map, table, n * kTile, n_all, j, ring + stage * kBuf, &full[stage],
-                is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
-      ++armed;
-      if (++stage == stages) stage = 0, phase ^= 1u;
-    }
-    // on an abort, let every load already issued land before the CTA leaves
-    if (*abort && lane == 0)
-      for (int n = max(0, armed - stages); n < armed; ++n) tc::mbar_drain(&full[n % stages], (n / stages) & 1, a.wait_ns);
-  } else if (warp >= 10) {
-    // ---------------- MMAs ----------------
-    const int s = warp - 10;
-    if (lane == 0) {
+  // The softmax threads hold a row's 128 scores: of the launch's 384 x 168
+  // registers 2 x 128 x 208 go to them, 128 x 88 stay with the others.
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 10) {
+      // ---------------- K and V tiles ----------------
+      const bool is_k = warp == 8;
+      const int stages = is_k ? kKStages : kVStages;
+      uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+      unsigned char* ring = smem + (is_k ? Layout::kK : Layout::kV);
+      const CUtensorMap* map = is_k ? &kmap : &vmap;
+      if (t.box > 0 && lane == 0) tc::tma_prefetch_map(map);
+      int stage = 0, armed = 0;
+      uint32_t phase = 0;
+      for (int n = t0; n < t1; ++n) {
+        const bool ok = tc::mbar_wait(&empty[stage], phase ^ 1u, abort, a.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        load_tile(t, is_k ? a.K : a.V, map, table, n * kTile, n_all, j, ring + stage * kBuf, &full[stage],
+                  is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
+        ++armed;
+        if (++stage == stages) stage = 0, phase ^= 1u;
+      }
+      // on an abort, let every load already issued land before the CTA leaves
+      if (*abort && lane == 0)
+        for (int n = max(0, armed - stages); n < armed; ++n) tc::mbar_drain(&full[n % stages], (n / stages) & 1, a.wait_ns);
+    } else if (lane == 0) {
+      // ---------------- MMAs ----------------
+      const int s = warp - 10;
       const uint32_t s_tmem = tmem + s * 256, o_tmem = s_tmem + kTile;
       const uint32_t q_addr = tc::smem_u32(smem + Layout::kQ + (both ? s : 0) * kBuf);
+      int done = 0;
       for (int n = t0; n < t1; ++n) {
         if (!is_mine(n, s)) continue;
         const int c = n - t0, ks = c % kKStages, vs = c % kVStages;
-        const bool seen = is_seen(n, s);
         if (!tc::mbar_wait(&k_full[ks], (c / kKStages) & 1, abort, a.wait_ns)) break;
-        if (!seen) {
+        if (!is_seen(n, s)) {
           tc::mbar_arrive(&k_empty[ks]);
           if (!tc::mbar_wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns)) break;
           tc::mbar_arrive(&v_empty[vs]);
@@ -363,15 +367,18 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       tc::mma_commit(&idle[s]);
       tc::mbar_drain(&idle[s], 0, a.wait_ns);
     }
-  } else if (both ? warp * 32 < nrows : (warp & 3) * 32 < nrows) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---------------- softmax: one row per thread ----------------
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256;
-    const uint32_t s_tmem = lane_base, o_tmem = lane_base + kTile;
+    const bool active = (both ? warp : warp & 3) * 32 < nrows;
+    const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
+    float m = -INFINITY, l = 0.f;
+    int done = 0;  // tiles that this slot has been through
     ScoreMap sm;
     sm.scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
     sm.cap = a.softcap * pa::kLog2e;
     sm.slope = a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
-    for (int n = t0; n < t1; ++n) {
+    for (int n = t0; active && n < t1; ++n) {
       if (!is_mine(n, slot) || !is_seen(n, slot)) continue;
       const bool ok = tc::mbar_wait(&s_full[slot], done & 1, abort, a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -455,70 +462,65 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     }
-  }
-
-  // ---- results ----
-  const uint32_t o_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256 + kTile;
-  float scale1 = 0.f;  // weight of the other slot's O, when it has the same rows
-  float* const other = reinterpret_cast<float*>(smem + Layout::kK);  // [128 columns][128 rows], then m, l
-  if (!both) {
-    tc::fence_before_sync();
-    __syncthreads();  // every MMA has finished: the tiles' memory is free
-    tc::fence_after_sync();
-    if (warp >= 4 && warp < 8 && (warp & 3) * 32 < nrows) {
-      other[kTile * kTile + row] = m, other[kTile * kTile + kTile + row] = l;
-      if (done > 0) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tc::tmem_ld32(o_tmem + 32 * k, o);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) other[(32 * k + i) * kTile + row] = __uint_as_float(o[i]);
+    // ---- results ----
+    float scale1 = 0.f;  // weight of the other slot's O, when it has the same rows
+    float* const other = reinterpret_cast<float*>(smem + Layout::kK);  // [128 columns][128 rows], then m, l
+    if (!both) {
+      softmax_barrier();  // every MMA has finished: the tiles' memory is free
+      if (slot == 1 && active) {
+        other[kTile * kTile + row] = m, other[kTile * kTile + kTile + row] = l;
+        if (done > 0) {
+  #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_tmem + 32 * k, o);
+            tc::tmem_wait_ld();
+  #pragma unroll
+            for (int i = 0; i < 32; ++i) other[(32 * k + i) * kTile + row] = __uint_as_float(o[i]);
+          }
         }
       }
+      softmax_barrier();
     }
-    __syncthreads();
-  }
-  const bool writes = both ? warp < 8 && warp * 32 < nrows : warp < 4 && warp * 32 < nrows;
-  if (writes && !*abort) {
-    float scale0 = 1.f;
-    if (!both) {
-      const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
-      const float top = fmaxf(m, m1);
-      scale0 = m == -INFINITY ? 0.f : pa::ex2(m - top);
-      scale1 = m1 == -INFINITY ? 0.f : pa::ex2(m1 - top);
-      l = l * scale0 + l1 * scale1, m = top;
-    }
-    const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
-    const bool partial = t.part0 >= 0;
-    const float inv = partial ? 1.f : l > 0.f ? 1.f / l : 0.f;
-    const int64_t part_row = partial ? (t.part0 + split) * a.T * a.Hq + out_row : 0;
-    if (live && partial) a.part_ml[part_row] = make_float2(m, l);
-    if (live && !partial && a.lse) a.lse[out_row] = l > 0.f ? (m + log2f(l)) * pa::kLn2 : -INFINITY;
-    const bool none = m == -INFINITY;  // nothing seen: O was never written, or is zero
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t o[32];
-      tc::tmem_ld32(o_tmem + 32 * k, o);
-      tc::tmem_wait_ld();
-      float x[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        x[i] = scale0 > 0.f ? __uint_as_float(o[i]) * scale0 : 0.f;
-        if (!both && scale1 > 0.f) x[i] = fmaf(other[(32 * k + i) * kTile + row], scale1, x[i]);
-        x[i] = none ? 0.f : x[i] * inv;
+    if (active && (both || slot == 0) && !*abort) {
+      float scale0 = 1.f;
+      if (!both) {
+        const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
+        const float top = fmaxf(m, m1);
+        scale0 = m == -INFINITY ? 0.f : pa::ex2(m - top);
+        scale1 = m1 == -INFINITY ? 0.f : pa::ex2(m1 - top);
+        l = l * scale0 + l1 * scale1, m = top;
       }
-      if (live && partial) {
-        float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * k);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-      } else if (live) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kHeadDim + 32 * k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                              pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+      const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
+      const bool partial = t.part0 >= 0;
+      const float inv = partial ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const int64_t part_row = partial ? (t.part0 + split) * a.T * a.Hq + out_row : 0;
+      if (live && partial) a.part_ml[part_row] = make_float2(m, l);
+      if (live && !partial && a.lse) a.lse[out_row] = l > 0.f ? (m + log2f(l)) * pa::kLn2 : -INFINITY;
+      const bool none = m == -INFINITY;  // nothing seen: O was never written, or is zero
+  #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t o[32];
+        tc::tmem_ld32(o_tmem + 32 * k, o);
+        tc::tmem_wait_ld();
+        float x[32];
+  #pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          x[i] = scale0 > 0.f ? __uint_as_float(o[i]) * scale0 : 0.f;
+          if (!both && scale1 > 0.f) x[i] = fmaf(other[(32 * k + i) * kTile + row], scale1, x[i]);
+          x[i] = none ? 0.f : x[i] * inv;
+        }
+        if (live && partial) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * k);
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kHeadDim + 32 * k);
+  #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+        }
       }
     }
   }
