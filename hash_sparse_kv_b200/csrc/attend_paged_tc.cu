@@ -108,6 +108,32 @@ struct ScoreMap {
   float cap;        // softcap * log2(e), 0 without a cap
   float slope;      // slope * log2(e)
 };
+// Bounded wait as tc::mbar_wait, but the clock (whose read takes longer than
+// most waits here) and the abort flag are looked at once in 64 tries.
+__device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (int i = 1;; ++i) {
+    if (tc::mbar_try_wait(b, parity)) return true;
+    if (i % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort) return false;
+      if (now - t0 > limit_ns) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ bool all(bool x) { return __all_sync(0xffffffffu, x); }
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Barrier of the two softmax warpgroups.
 __device__ __forceinline__ void softmax_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -226,7 +252,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   uint64_t* p_full = s_full + 2;              // [slot] P in tensor memory, O rescaled
   uint64_t* o_done = p_full + 2;              // [slot] O holds the tile
   uint64_t* idle = o_done + 2;                // [slot] every MMA issued has finished
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(idle + 2);
+  uint64_t* turn = idle + 2;                  // [slot] the other slot is through with its exponentials
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* range = reinterpret_cast<int*>(tmem_slot + 2);  // [slot][lo, hi]
 
@@ -247,9 +274,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     for (int i = 0; i < 2; ++i) {
       const int rows = both ? min(kTile, nrows - i * kTile) : nrows;
       tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&p_full[i], (rows + 31) / 32 * 32);  // warps without a row take no part
+      tc::mbar_init(&p_full[i], (rows + 31) / 32);  // a warp each; those without a row take no part
       tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&idle[i], 1);
+      tc::mbar_init(&turn[1 - i], (rows + 31) / 32);  // a warp of slot i each
       range[2 * i] = INT32_MAX, range[2 * i + 1] = 0;
     }
     *abort = 0;
@@ -318,8 +346,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       int stage = 0, armed = 0;
       uint32_t phase = 0;
       for (int n = t0; n < t1; ++n) {
-        const bool ok = tc::mbar_wait(&empty[stage], phase ^ 1u, abort, a.wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!all(wait(&empty[stage], phase ^ 1u, abort, a.wait_ns))) break;
         load_tile(t, is_k ? a.K : a.V, map, table, n * kTile, n_all, j, ring + stage * kBuf, &full[stage],
                   is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
         ++armed;
@@ -328,44 +355,59 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       // on an abort, let every load already issued land before the CTA leaves
       if (*abort && lane == 0)
         for (int n = max(0, armed - stages); n < armed; ++n) tc::mbar_drain(&full[n % stages], (n / stages) & 1, a.wait_ns);
-    } else if (lane == 0) {
+    } else {
       // ---------------- MMAs ----------------
-      const int s = warp - 10;
-      const uint32_t s_tmem = tmem + s * 256, o_tmem = s_tmem + kTile;
-      const uint32_t q_addr = tc::smem_u32(smem + Layout::kQ + (both ? s : 0) * kBuf);
+      // the whole warp goes through the loop and one elected thread issues, so
+      // that addresses and descriptors stay in uniform registers (issued from a
+      // branch of one lane, eight MMAs took 800 cycles instead of 512)
+      const int s = __shfl_sync(0xffffffffu, warp, 0) - 10;
+      const uint32_t s_tmem = __shfl_sync(0xffffffffu, tmem, 0) + s * 256, o_tmem = s_tmem + kTile;
+      const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(smem + Layout::kQ) + (both ? s : 0) * kBuf);
+      const uint64_t k_desc0 = tc::sw128_desc(tc::smem_u32(smem + Layout::kK));
+      const uint64_t v_desc0 = sw128_desc_mn(tc::smem_u32(smem + Layout::kV), kHalf);
       int done = 0;
       for (int n = t0; n < t1; ++n) {
         if (!is_mine(n, s)) continue;
         const int c = n - t0, ks = c % kKStages, vs = c % kVStages;
-        if (!tc::mbar_wait(&k_full[ks], (c / kKStages) & 1, abort, a.wait_ns)) break;
+        if (!all(wait(&k_full[ks], (c / kKStages) & 1, abort, a.wait_ns))) break;
         if (!is_seen(n, s)) {
-          tc::mbar_arrive(&k_empty[ks]);
-          if (!tc::mbar_wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns)) break;
-          tc::mbar_arrive(&v_empty[vs]);
+          if (lane == 0) tc::mbar_arrive(&k_empty[ks]);
+          if (!all(wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns))) break;
+          if (lane == 0) tc::mbar_arrive(&v_empty[vs]);
           continue;
         }
         tc::fence_after_sync();
-        const uint32_t k_addr = tc::smem_u32(smem + Layout::kK + ks * kBuf);
         // S of this tile overwrites the last tile's P: MMAs of one thread run in order
+        if (elected()) {
+          const uint64_t k_desc = k_desc0 + ks * (kBuf >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16(s_tmem, tc::sw128_desc(q_addr + (kk >> 2) * kHalf + (kk & 3) * 32),
-                       tc::sw128_desc(k_addr + (kk >> 2) * kHalf + (kk & 3) * 32), kIdescS, kk != 0);
-        tc::mma_commit(&s_full[s]);
-        tc::mma_commit(&k_empty[ks]);
-        if (!tc::mbar_wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns)) break;
-        if (!tc::mbar_wait(&p_full[s], done & 1, abort, a.wait_ns)) break;
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            tc::mma_bf16(s_tmem, q_desc + at, k_desc + at, kIdescS, kk != 0);
+          }
+          tc::mma_commit(&s_full[s]);
+          tc::mma_commit(&k_empty[ks]);
+        }
+        __syncwarp();
+        if (!all(wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns))) break;
+        if (!all(wait(&p_full[s], done & 1, abort, a.wait_ns))) break;
         tc::fence_after_sync();
-        const uint32_t v_addr = tc::smem_u32(smem + Layout::kV + vs * kBuf);
+        if (elected()) {
+          const uint64_t v_desc = v_desc0 + vs * (kBuf >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(o_tmem, s_tmem + kk * 8, sw128_desc_mn(v_addr + kk * 16 * 128, kHalf), kIdescO, (done | kk) != 0);
-        tc::mma_commit(&v_empty[vs]);
-        tc::mma_commit(&o_done[s]);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ts(o_tmem, s_tmem + kk * 8, v_desc + kk * (16 * 128 >> 4), kIdescO, (done | kk) != 0);
+          tc::mma_commit(&v_empty[vs]);
+          tc::mma_commit(&o_done[s]);
+        }
+        __syncwarp();
         ++done;
       }
-      tc::mma_commit(&idle[s]);
-      tc::mbar_drain(&idle[s], 0, a.wait_ns);
+      if (elected()) {
+        tc::mma_commit(&idle[s]);
+        tc::mbar_drain(&idle[s], 0, a.wait_ns);
+      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -374,13 +416,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
     float m = -INFINITY, l = 0.f;
     int done = 0;  // tiles that this slot has been through
+    // tiles that both slots go through: for these they take turns
+    int mine = 0, theirs = 0;
+    for (int n = t0; n < t1; ++n) {
+      mine += is_mine(n, slot) && is_seen(n, slot);
+      theirs += is_mine(n, 1 - slot) && is_seen(n, 1 - slot);
+    }
+    const int turns = min(mine, theirs);
     ScoreMap sm;
     sm.scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
     sm.cap = a.softcap * pa::kLog2e;
     sm.slope = a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
     for (int n = t0; active && n < t1; ++n) {
       if (!is_mine(n, slot) || !is_seen(n, slot)) continue;
-      const bool ok = tc::mbar_wait(&s_full[slot], done & 1, abort, a.wait_ns);
+      const bool ok = wait(&s_full[slot], done & 1, abort, a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after_sync();
       uint32_t v[4][32];
@@ -423,7 +472,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         float f = 1.f;
         if (grown) f = pa::ex2(m - top), l *= f, m = top;  // m = -inf: 0
         if (done > 0) {
-          const bool ok2 = tc::mbar_wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
+          const bool ok2 = wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
           if (!__all_sync(0xffffffffu, ok2)) break;
           tc::fence_after_sync();
 #pragma unroll
@@ -436,6 +485,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             tmem_st32(o_tmem + 32 * k, o);
           }
         }
+      }
+      // One slot's exponentials at a time: together they would take as long, and
+      // the tensor cores would wait for both instead of working for the other.
+      if (done < turns && (slot == 1 || done > 0)) {
+        const bool ok3 = wait(&turn[slot], (slot == 1 ? done : done - 1) & 1, abort, a.wait_ns);
+        if (!__all_sync(0xffffffffu, ok3)) break;
       }
       const float off = m == -INFINITY ? 0.f : m;
       float sum[2] = {0.f, 0.f};
@@ -452,13 +507,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         tmem_st16(s_tmem + 16 * k, p);
       }
       l += sum[0] + sum[1];
+      __syncwarp();
+      if (done < turns && lane == 0) tc::mbar_arrive(&turn[1 - slot]);
       tmem_wait_st();
       tc::fence_before_sync();
-      tc::mbar_arrive(&p_full[slot]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&p_full[slot]);
       ++done;
     }
     if (done > 0) {
-      const bool ok = tc::mbar_wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
+      const bool ok = wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
       __all_sync(0xffffffffu, ok);
       tc::fence_after_sync();
     }
