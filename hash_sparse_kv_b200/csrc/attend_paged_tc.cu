@@ -21,6 +21,7 @@
 // 10 and 11: the MMAs of slot 0 and 1.
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include "attend_paged.cuh"
 #include "tc.cuh"
@@ -36,6 +37,7 @@ constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kHalf = kTile * 128;     // 128 rows x 64 bf16
 constexpr uint32_t kBuf = 2 * kHalf;
 constexpr int kMaskRing = 8;                // tiles whose valid-token masks are kept
+constexpr uint32_t kPolyMask = 0x11;        // of eight pairs of exponentials, those taken by the polynomial
 constexpr float kGrowth = 8.f;              // rescale when the maximum grows by more than 2^8
 
 struct Layout {
@@ -96,18 +98,77 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Two fp32 values side by side: one instruction works on both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 2^x for two x in [-126, 8] without the special-function unit, whose 16
+// results a cycle are what a softmax of this shape waits for (128 x 128
+// exponentials take it as long as the tensor cores need for the tile's
+// products).  x = n + f, n the nearest integer (read off the low bits of
+// x + 1.5 * 2^23), 2^f by the degree-4 minimax polynomial on [-1/2, 1/2]
+// (relative error 2.7e-6), n added to the exponent.
+__device__ __forceinline__ float2 exp2_poly(uint64_t x) {
+  const float kMagic = 12582912.f;
+  const uint64_t r = add2(x, pair(kMagic, kMagic));
+  const uint64_t f = fma2(add2(r, pair(-kMagic, -kMagic)), pair(-1.f, -1.f), x);
+  uint64_t p = fma2(pair(9.570102207e-03f, 9.570102207e-03f), f, pair(5.591786280e-02f, 5.591786280e-02f));
+  p = fma2(p, f, pair(2.402474433e-01f, 2.402474433e-01f));
+  p = fma2(p, f, pair(6.931217909e-01f, 6.931217909e-01f));
+  p = fma2(p, f, pair(9.999992847e-01f, 9.999992847e-01f));
+  const float2 n = unpair(r), v = unpair(p);
+  return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(n.x) << 23)),
+                     __int_as_float(__float_as_int(v.y) + (__float_as_int(n.y) << 23)));
+}
+// tanh on [-1, 1] for two values: odd minimax polynomial of degree 13,
+// absolute error 1e-7.
+__device__ __forceinline__ uint64_t tanh_poly(uint64_t x) {
+  const float c[7] = {9.999997020e-01f, -3.333213031e-01f, 1.331958324e-01f, -5.326583236e-02f,
+                      1.997327618e-02f, -5.951274652e-03f, 9.637702024e-04f};
+  const uint64_t u = mul2(x, x);
+  uint64_t p = pair(c[6], c[6]);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) p = fma2(p, u, pair(c[i], c[i]));
+  return mul2(p, x);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// Both score maps in units of log2(e).
-struct ScoreMap {
-  float scale;      // scale * log2(e), or scale / softcap with a cap
-  float cap;        // softcap * log2(e), 0 without a cap
-  float slope;      // slope * log2(e)
-};
 // Bounded wait as tc::mbar_wait, but the clock (whose read takes longer than
 // most waits here) and the abort flag are looked at once in 64 tries.
 __device__ __forceinline__ bool wait(uint64_t* b, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
@@ -233,7 +294,17 @@ __device__ __forceinline__ void load_tile(const TcArgs& t, const void* pool, con
   if (lane == 0) tc::mbar_arrive(bar);
 }
 
-template <bool kPrefix, bool kGeneral>
+// A slot's tiles: every step-th from first up to last.
+struct Run {
+  int first, last, step;
+  __device__ __forceinline__ int count() const { return last > first ? (last - first + step - 1) / step : 0; }
+};
+
+// How scores are formed: scaled only; capped too; with a bias by distance (and
+// a cap or a scale of any sign).
+enum { kPlain = 0, kCapped = 1, kBiased = 2 };
+
+template <bool kPrefix, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ TcArgs t) {
@@ -250,7 +321,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   uint64_t* v_empty = v_full + kVStages;
   uint64_t* s_full = v_empty + kVStages;      // [slot] S in tensor memory
   uint64_t* p_full = s_full + 2;              // [slot] P in tensor memory, O rescaled
-  uint64_t* o_done = p_full + 2;              // [slot] O holds the tile
+  uint64_t* p_half = p_full + 2;              // [slot] the same for the first 64 tokens
+  uint64_t* o_done = p_half + 2;              // [slot] O holds the tile
   uint64_t* idle = o_done + 2;                // [slot] every MMA issued has finished
   uint64_t* turn = idle + 2;                  // [slot] the other slot is through with its exponentials
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
@@ -275,6 +347,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const int rows = both ? min(kTile, nrows - i * kTile) : nrows;
       tc::mbar_init(&s_full[i], 1);
       tc::mbar_init(&p_full[i], (rows + 31) / 32);  // a warp each; those without a row take no part
+      tc::mbar_init(&p_half[i], (rows + 31) / 32);
       tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&idle[i], 1);
       tc::mbar_init(&turn[1 - i], (rows + 31) / 32);  // a warp of slot i each
@@ -327,14 +400,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int per = (last - first + t.splits - 1) / t.splits;
   const int t0 = first + split * per, t1 = min(last, t0 + per);
 
-  // the tiles that slot s works on: whether tile n is one of them
-  auto is_mine = [&](int n, int s) { return both || ((n - t0) & 1) == s; };
-  auto is_seen = [&](int n, int s) { return !both || (n >= range[2 * s] / kTile && n * kTile < range[2 * s + 1]); };
+  // the tiles that a slot works on
+  auto run_of = [&](int s) -> Run {
+    if (!both) return Run{t0 + s, t1, 2};
+    return Run{max(t0, range[2 * s] / kTile), min(t1, (range[2 * s + 1] + kTile - 1) / kTile), 1};
+  };
 
   // The softmax threads hold a row's 128 scores: of the launch's 384 x 168
-  // registers 2 x 128 x 208 go to them, 128 x 88 stay with the others.
+  // registers 2 x 128 x 200 go to them, 128 x 104 stay with the others.
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp < 10) {
       // ---------------- K and V tiles ----------------
       const bool is_k = warp == 8;
@@ -365,44 +440,75 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(smem + Layout::kQ) + (both ? s : 0) * kBuf);
       const uint64_t k_desc0 = tc::sw128_desc(tc::smem_u32(smem + Layout::kK));
       const uint64_t v_desc0 = sw128_desc_mn(tc::smem_u32(smem + Layout::kV), kHalf);
-      int done = 0;
-      for (int n = t0; n < t1; ++n) {
-        if (!is_mine(n, s)) continue;
-        const int c = n - t0, ks = c % kKStages, vs = c % kVStages;
-        if (!all(wait(&k_full[ks], (c / kKStages) & 1, abort, a.wait_ns))) break;
-        if (!is_seen(n, s)) {
+      const Run run = run_of(s);
+      int done = 0, ks = 0, vs = 0;
+      uint32_t kph = 0, vph = 0;
+      auto advance = [&](int by) {
+        if ((ks += by) >= kKStages) ks -= kKStages, kph ^= 1u;
+        if ((vs += by) >= kVStages) vs -= kVStages, vph ^= 1u;
+      };
+      // tiles that only the other slot needs are given back as they come
+      auto pass = [&](int from, int to) -> bool {
+        for (int n = from; n < to; ++n) {
+          if (!all(wait(&k_full[ks], kph, abort, a.wait_ns))) return false;
           if (lane == 0) tc::mbar_arrive(&k_empty[ks]);
-          if (!all(wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns))) break;
+          if (!all(wait(&v_full[vs], vph, abort, a.wait_ns))) return false;
           if (lane == 0) tc::mbar_arrive(&v_empty[vs]);
-          continue;
+          advance(1);
         }
-        tc::fence_after_sync();
-        // S of this tile overwrites the last tile's P: MMAs of one thread run in order
-        if (elected()) {
-          const uint64_t k_desc = k_desc0 + ks * (kBuf >> 4);
+        return true;
+      };
+      bool ok = true;
+      if (both)
+        ok = pass(t0, min(t1, run.first));
+      else if (s == 1)
+        advance(1);
+      auto issue_s = [&](int stage) {
+        const uint64_t k_desc = k_desc0 + stage * (kBuf >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-            tc::mma_bf16(s_tmem, q_desc + at, k_desc + at, kIdescS, kk != 0);
-          }
-          tc::mma_commit(&s_full[s]);
-          tc::mma_commit(&k_empty[ks]);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+          tc::mma_bf16(s_tmem, q_desc + at, k_desc + at, kIdescS, kk != 0);
+        }
+        tc::mma_commit(&s_full[s]);
+        tc::mma_commit(&k_empty[stage]);
+      };
+      if (ok && run.first < run.last) {
+        ok = all(wait(&k_full[ks], kph, abort, a.wait_ns));
+        tc::fence_after_sync();
+        if (ok && elected()) issue_s(ks);
+        __syncwarp();
+      }
+      for (int n = run.first; ok && n < run.last; n += run.step) {
+        const int v_at = vs;
+        if (!(ok = all(wait(&v_full[vs], vph, abort, a.wait_ns)))) break;
+        advance(run.step);
+        const bool more = n + run.step < run.last;
+        if (more && !(ok = all(wait(&k_full[ks], kph, abort, a.wait_ns)))) break;
+        const uint64_t v_desc = v_desc0 + v_at * (kBuf >> 4);
+        if (!(ok = all(wait(&p_half[s], done & 1, abort, a.wait_ns)))) break;
+        tc::fence_after_sync();
+        if (elected()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(o_tmem, s_tmem + kk * 8, v_desc + kk * (16 * 128 >> 4), kIdescO, (done | kk) != 0);
         }
         __syncwarp();
-        if (!all(wait(&v_full[vs], (c / kVStages) & 1, abort, a.wait_ns))) break;
-        if (!all(wait(&p_full[s], done & 1, abort, a.wait_ns))) break;
+        if (!(ok = all(wait(&p_full[s], done & 1, abort, a.wait_ns)))) break;
         tc::fence_after_sync();
         if (elected()) {
-          const uint64_t v_desc = v_desc0 + vs * (kBuf >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(o_tmem, s_tmem + kk * 8, v_desc + kk * (16 * 128 >> 4), kIdescO, (done | kk) != 0);
-          tc::mma_commit(&v_empty[vs]);
+          for (int kk = 4; kk < 8; ++kk)
+            mma_bf16_ts(o_tmem, s_tmem + kk * 8, v_desc + kk * (16 * 128 >> 4), kIdescO, 1u);
+          tc::mma_commit(&v_empty[v_at]);
           tc::mma_commit(&o_done[s]);
+          // the next tile's S overwrites this one's P: MMAs of one thread run in order
+          if (more) issue_s(ks);
         }
         __syncwarp();
         ++done;
       }
+      if (ok && both) pass(max(run.last, run.first), t1);
       if (elected()) {
         tc::mma_commit(&idle[s]);
         tc::mbar_drain(&idle[s], 0, a.wait_ns);
@@ -410,63 +516,93 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------- softmax: one row per thread ----------------
     const bool active = (both ? warp : warp & 3) * 32 < nrows;
     const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
     float m = -INFINITY, l = 0.f;
     int done = 0;  // tiles that this slot has been through
-    // tiles that both slots go through: for these they take turns
-    int mine = 0, theirs = 0;
-    for (int n = t0; n < t1; ++n) {
-      mine += is_mine(n, slot) && is_seen(n, slot);
-      theirs += is_mine(n, 1 - slot) && is_seen(n, 1 - slot);
-    }
-    const int turns = min(mine, theirs);
-    ScoreMap sm;
-    sm.scale = a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
-    sm.cap = a.softcap * pa::kLog2e;
-    sm.slope = a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
-    for (int n = t0; active && n < t1; ++n) {
-      if (!is_mine(n, slot) || !is_seen(n, slot)) continue;
+    const Run run = run_of(slot), other_run = run_of(1 - slot);
+    const int turns = min(run.count(), other_run.count());  // tiles for which the slots take turns
+    // a score in units of log2(e) is value * c: value is q.k, or its tanh, or
+    // (biased) the score itself
+    const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f, cap = a.softcap * pa::kLog2e;
+    const float c = kMode == kPlain ? a.scale * pa::kLog2e : kMode == kCapped ? cap : 1.f;
+    const float slope = kMode == kBiased && a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
+    for (int n = run.first; active && n < run.last; n += run.step) {
       const bool ok = wait(&s_full[slot], done & 1, abort, a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc::fence_after_sync();
-      uint32_t v[4][32];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) tc::tmem_ld32(s_tmem + 32 * k, v[k]);
-      tc::tmem_wait_ld();
       const int u0 = n * kTile;
-      if constexpr (kGeneral) {
-        const float d0 = (float)(sp.pos - u0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float z = __uint_as_float(v[k][i]) * sm.scale;
-            if (sm.cap > 0.f) z = pa::capped(z, sm.cap);
-            v[k][i] = __float_as_uint(fmaf(-sm.slope, fabsf(d0 - (float)(32 * k + i)), z));
-          }
-      }
       const uint4 there = valid_s[(n - t0) % kMaskRing];
       const bool whole = sp.lo <= u0 && sp.hi >= u0 + kTile && (there.x & there.y & there.z & there.w) == ~0u;
-      if (__any_sync(0xffffffffu, !whole)) {
+      const bool masked = __any_sync(0xffffffffu, !whole);
+      // Scores that are more than a multiple of the products are formed first
+      // and go back to tensor memory.  Loops over 32 columns stay rolled: a
+      // row's 128 scores in registers meant spills and code that the
+      // instruction cache could not hold, and reading them again is cheap.
+      auto form = [&] {
+        const float d0 = (float)(sp.pos - u0);
         const uint32_t w[4] = {there.x, there.y, there.z, there.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v[32];
+          tc::tmem_ld32(s_tmem + 32 * k, v);
+          tc::tmem_wait_ld();
+          const uint32_t in = k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3];
+          const int lo = min(max(sp.lo - u0 - 32 * k, 0), 32), hi = min(max(sp.hi - u0 - 32 * k, 0), 32);
+          // bit i: token i is seen
+          const uint32_t see = masked ? in & (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1) : ~0u;
+          const float d = d0 - (float)(32 * k);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int u = u0 + 32 * k + i;
-            if (u < sp.lo || u >= sp.hi || !(w[k] >> i & 1u)) v[k][i] = 0xff800000u;  // -inf
+            float z = __uint_as_float(v[i]);
+            if (kMode == kCapped) z = pa::capped(z * to_cap, 1.f);
+            if (kMode == kBiased) {
+              z = cap > 0.f ? pa::capped(z * to_cap, cap) : z * (a.scale * pa::kLog2e);
+              z = fmaf(-slope, fabsf(d - (float)i), z);
+            }
+            v[i] = see >> i & 1u ? __float_as_uint(z) : 0xff800000u;  // -inf
           }
+          tmem_st32(s_tmem + 32 * k, v);
+        }
+        tmem_wait_st();
+      };
+      bool formed = kMode == kBiased || masked;
+      if (formed) form();
+      float top, low;
+      auto extremes = [&] {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          uint32_t v[2][32];
+          tc::tmem_ld32(s_tmem + 32 * k, v[0]);
+          tc::tmem_ld32(s_tmem + 32 * k + 32, v[1]);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int q = h * 2 + (i >> 1 & 1);
+              mx[q] = max3(mx[q], __uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]));
+              if (kMode == kCapped) mn[q] = min3(mn[q], __uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]));
+            }
+        }
+        top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), low = fminf(min3(mn[0], mn[1], mn[2]), mn[3]);
+      };
+      extremes();
+      if constexpr (kMode == kCapped) {
+        // the polynomial serves while no score of the warp is past the cap
+        if (!formed && !all(fmaxf(top, -low) * fabsf(to_cap) <= 1.f)) {
+          form(), formed = true;
+          extremes();
+        }
+        if (!formed) {
+          const float t = to_cap > 0.f ? top : low;
+          top = unpair(tanh_poly(pair(t * to_cap, 0.f))).x;
+        }
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(v[k][i]));
-      const float c = kGeneral ? 1.f : sm.scale;  // positive: the largest product is the largest score
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      top *= c;  // c is positive: the largest value is the largest score
       const bool grown = top > m + kGrowth || (m == -INFINITY && top > -INFINITY);
       if (__any_sync(0xffffffffu, grown)) {
         float f = 1.f;
@@ -493,20 +629,53 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (!__all_sync(0xffffffffu, ok3)) break;
       }
       const float off = m == -INFINITY ? 0.f : m;
-      float sum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      uint64_t sum[2] = {0, 0};
+      const uint64_t c2 = pair(c, c), off2 = pair(-off, -off);
+      const uint64_t cap2 = pair(to_cap, to_cap);
+      // 32 scores to weights
+      auto weigh = [&](const uint32_t(&v)[32], int k, auto raw) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float x = pa::ex2(fmaf(__uint_as_float(v[k][2 * i]), c, -off));
-          const float y = pa::ex2(fmaf(__uint_as_float(v[k][2 * i + 1]), c, -off));
-          sum[0] += x, sum[1] += y;
-          p[i] = pack_bf16(x, y);
+          uint64_t z = pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+          if constexpr (decltype(raw)::value) z = tanh_poly(mul2(z, cap2));
+          float2 x = unpair(fma2(z, c2, off2));
+          if (kPolyMask >> (i % 8) & 1)  // a masked score comes out as 2^-126
+            x = exp2_poly(pair(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
+          else
+            x = make_float2(pa::ex2(x.x), pa::ex2(x.y));
+          sum[i & 1] = add2(sum[i & 1], pair(x.x, x.y));
+          p[i] = pack_bf16(x.x, x.y);
         }
-        tmem_st16(s_tmem + 16 * k, p);
-      }
-      l += sum[0] + sum[1];
+        tmem_st16(s_tmem + 16 * k, p);  // behind the columns still to be read
+      };
+      auto weigh_all = [&](auto raw) {
+        // the next 32 columns are on their way while these are weighed
+        uint32_t va[32], vb[32], vc[32], vd[32];
+        tc::tmem_ld32(s_tmem, va);
+        tc::tmem_wait_ld();
+        tc::tmem_ld32(s_tmem + 32, vb);
+        weigh(va, 0, raw);
+        tc::tmem_wait_ld();
+        tc::tmem_ld32(s_tmem + 64, vc);
+        weigh(vb, 1, raw);
+        tc::tmem_wait_ld();
+        // P V may start on these 64 tokens
+        tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_half[slot]);
+        tc::tmem_ld32(s_tmem + 96, vd);
+        weigh(vc, 2, raw);
+        tc::tmem_wait_ld();
+        weigh(vd, 3, raw);
+      };
+      if (kMode == kCapped && !formed)
+        weigh_all(std::true_type{});
+      else
+        weigh_all(std::false_type{});
+      const float2 both_sums = unpair(add2(sum[0], sum[1]));
+      l += both_sums.x + both_sums.y;
       __syncwarp();
       if (done < turns && lane == 0) tc::mbar_arrive(&turn[1 - slot]);
       tmem_wait_st();
@@ -551,11 +720,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
       const bool partial = t.part0 >= 0;
-      const float inv = partial ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const bool none = m == -INFINITY;  // nothing seen: O was never written, or means nothing
+      const float inv = partial ? 1.f : none ? 0.f : 1.f / l;
       const int64_t part_row = partial ? (t.part0 + split) * a.T * a.Hq + out_row : 0;
-      if (live && partial) a.part_ml[part_row] = make_float2(m, l);
-      if (live && !partial && a.lse) a.lse[out_row] = l > 0.f ? (m + log2f(l)) * pa::kLn2 : -INFINITY;
-      const bool none = m == -INFINITY;  // nothing seen: O was never written, or is zero
+      if (live && partial) a.part_ml[part_row] = make_float2(m, none ? 0.f : l);
+      if (live && !partial && a.lse) a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * pa::kLn2;
   #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t o[32];
@@ -684,9 +853,10 @@ int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int s
     if (rc != HKV_OK) return rc;
     t.box = box;
   }
-  const bool general = a.softcap > 0.f || a.slopes != nullptr || !(a.scale > 0.f);
-  auto kernel = prefix ? (general ? attend_tc_kernel<true, true> : attend_tc_kernel<true, false>)
-                       : (general ? attend_tc_kernel<false, true> : attend_tc_kernel<false, false>);
+  const int mode = a.slopes != nullptr || (!(a.scale > 0.f) && a.softcap == 0.f) ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
+  auto kernel = mode == kBiased ? (prefix ? attend_tc_kernel<true, kBiased> : attend_tc_kernel<false, kBiased>)
+                : mode == kCapped ? (prefix ? attend_tc_kernel<true, kCapped> : attend_tc_kernel<false, kCapped>)
+                                  : (prefix ? attend_tc_kernel<true, kPlain> : attend_tc_kernel<false, kPlain>);
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return cuda_check(e, "attention smem attribute");
   const int64_t grid = (int64_t)t.tiles * splits * p.Hkv;
