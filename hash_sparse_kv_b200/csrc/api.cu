@@ -473,7 +473,7 @@ int hkv_append_paged(const hkv_hash* hash, int dtype, const hkv_rope* rope, int 
   return launch_append_paged(p, pm, ws, static_cast<cudaStream_t>(stream));
 }
 
-// Positions are 32-bit in the kernels, a tile of them past the last included.
+// Positions and rows are 32-bit in the kernels, a tile of them past the last included.
 constexpr int64_t kMaxAttendTokens = INT32_MAX - 255;
 
 // What both dense attention calls check; `p` is filled as far as they share it.
@@ -482,7 +482,8 @@ static int check_attend(int B, int64_t T, int Hq, int Hkv, int dtype, float scal
   int rc = check_heads(B, Hq, Hkv);
   if (rc == HKV_OK) rc = check_dtype(dtype);
   if (rc != HKV_OK) return rc;
-  if (T < 0 || T > INT32_MAX) return fail(HKV_ERR_INVALID_ARG, "T %lld", (long long)T);
+  if (T < 0) return fail(HKV_ERR_INVALID_ARG, "T %lld", (long long)T);
+  if (T > kMaxAttendTokens / Hq) return fail(HKV_ERR_UNSUPPORTED, "T * Hq > 2^31 - 256");
   if (Hkv > 65535) return fail(HKV_ERR_UNSUPPORTED, "Hkv %d > 65535", Hkv);
   if (!std::isfinite(scale)) return fail(HKV_ERR_INVALID_ARG, "scale is not finite");
   p = PagedAttend{};

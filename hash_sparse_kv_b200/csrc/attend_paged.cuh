@@ -72,14 +72,15 @@ struct Span {
 };
 // Positions seen by new token i of sequence b (prefill: the own pages hold the
 // whole sequence).
-__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i) {
+// `docs`: whether q_first counts.
+__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i, bool docs = true) {
   Span r;
   // a call may hold more new tokens than the clamped length: positions below
   // zero see nothing but a prefix
   const int64_t p = s.n - s.n_new + i;
   int64_t lo = 0, hi = p + 1;
   if (a.window > 0 && p + 1 - a.window > lo) lo = p + 1 - a.window;
-  if (a.q_first) {
+  if (docs && a.q_first) {
     const int64_t f = a.q_first[s.first + i];
     lo = f > lo ? f : lo;
   }
@@ -96,10 +97,11 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int6
 
 // Pool row (of KV head j) that holds token u behind `table`, -1 for a page
 // outside the pool.
-__device__ __forceinline__ int64_t pool_row(const Args& a, const int32_t* __restrict__ table, int64_t u, int j) {
-  const int64_t page = table[u / a.pm.page_size];
+__device__ __forceinline__ int64_t pool_row(const Args& a, const int32_t* __restrict__ table, uint32_t u, int j) {
+  const uint32_t P = a.pm.page_size, at = u / P;
+  const int64_t page = table[at];
   if (page < 0 || page >= a.pm.num_pages) return -1;
-  return (page * a.Hkv + j) * a.pm.page_size + u % a.pm.page_size;
+  return (page * a.Hkv + j) * P + (u - at * P);
 }
 
 __device__ __forceinline__ float ex2(float x) {

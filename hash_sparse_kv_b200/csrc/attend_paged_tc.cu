@@ -97,6 +97,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Values from tensor memory are there after the wait only: the empty
+// statements make every later use depend on it.
+template <int N>
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[N]) {
+  tc::tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Two fp32 values side by side: one instruction works on both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -239,7 +247,7 @@ __device__ __forceinline__ void load_tile(const TcArgs& t, const void* pool, con
                                           const int32_t* __restrict__ table, int u0, int n, int j, unsigned char* dst,
                                           uint64_t* bar, uint4* valid) {
   const Args& a = t.a;
-  const int lane = threadIdx.x & 31, P = a.pm.page_size;
+  const int lane = threadIdx.x & 31;
   if (t.box > 0 && u0 + kTile <= n) {
     const int boxes = kTile / t.box;  // at most 16
     int64_t row = 0;
@@ -325,9 +333,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   uint64_t* o_done = p_half + 2;              // [slot] O holds the tile
   uint64_t* idle = o_done + 2;                // [slot] every MMA issued has finished
   uint64_t* turn = idle + 2;                  // [slot] the other slot is through with its exponentials
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 2);
+  uint64_t* q_full = turn + 2;                // [slot] queries in shared memory
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 2);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* range = reinterpret_cast<int*>(tmem_slot + 2);  // [slot][lo, hi]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int j = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv;
@@ -351,60 +359,52 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&idle[i], 1);
       tc::mbar_init(&turn[1 - i], (rows + 31) / 32);  // a warp of slot i each
-      range[2 * i] = INT32_MAX, range[2 * i + 1] = 0;
+      tc::mbar_init(&q_full[i], (rows + 31) / 32);
     }
     *abort = 0;
     tc::mbar_init_fence();
   }
   if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
-  __syncthreads();
-
-  // ---- rows: queries to shared memory, what each row sees ----
-  const int slot = warp >> 2;  // of the softmax warps
-  const int row = both ? threadIdx.x : (threadIdx.x & (kTile - 1));
-  const bool live = warp < 8 && row < nrows;
-  const int64_t tok = (r0 + row) / a.g;
-  const int head = (int)((r0 + row) % a.g);
-  pa::Span sp{0, INT32_MAX, 0};  // rows that are only padding see everything: no masks for their sake
-  if (live) {
+  // What a slot's rows see together, a bound rather than the exact union:
+  // positions grow with the rows.  Every warp works it out for itself.
+  const int g = a.g, row_base = (int)r0;  // r0 + 255 < T * g < 2^31
+  auto seen_by = [&](int s, int& lo, int& hi) {
     if constexpr (kPrefix) {
-      const int64_t n = min((int64_t)max(a.n_tok[tok], 0), a.n_max);
-      sp = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
+      lo = 0, hi = (int)a.n_prefix;
     } else {
-      sp = pa::span_of(a, seq, b, tok);
+      const int ra = both ? s * kTile : 0, rb = min(nrows, ra + kTile) - 1;
+      const int ia = (row_base + ra) / g, ib = (row_base + rb) / g;
+      const pa::Span x = pa::span_of(a, seq, b, ia, false), y = pa::span_of(a, seq, b, ib, false);
+      lo = x.lo, hi = y.hi;
+      if (a.q_first) {
+        int f = INT32_MAX;
+        for (int i = ia + lane; i <= ib; i += 32) f = min(f, __ldg(a.q_first + seq.first + i));
+        lo = max(lo, __reduce_min_sync(0xffffffffu, f));
+      }
+      lo = min(lo, hi);
     }
-    if (sp.lo < sp.hi) {
-      atomicMin(&range[2 * slot], sp.lo);
-      atomicMax(&range[2 * slot + 1], sp.hi);
-    }
-  }
-  if (warp < (both ? 8 : 4)) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (seq.first + tok) * a.q_stride + (int64_t)(j * a.g + head) * kHeadDim;
-    unsigned char* dst = smem + Layout::kQ + (row >> 7) * kBuf + (row & 127) * 128;
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const uint4 v = live ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + (((c & 7) ^ (row & 7)) << 4)) = v;
-    }
-    async_fence();
-  }
+  };
+  int lo0, hi0, lo1, hi1;
+  seen_by(0, lo0, hi0);
+  seen_by(1, lo1, hi1);
+  const int n_all = kPrefix ? (int)a.n_prefix : (int)seq.n;
+  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)b * a.pm.max_pages;
+  // tiles of the CTA, then this split's run of them
+  const int lo = hi0 <= lo0 ? lo1 : hi1 <= lo1 ? lo0 : min(lo0, lo1), hi = max(hi0 > lo0 ? hi0 : 0, hi1 > lo1 ? hi1 : 0);
+  const int first = lo < hi ? lo / kTile : 0, last = lo < hi ? (hi + kTile - 1) / kTile : 0;
+  const int per = (last - first + t.splits - 1) / t.splits;
+  const int t0 = first + split * per, t1 = min(last, t0 + per);
+  // the tiles that a slot works on
+  auto run_of = [&](int s) -> Run {
+    if (!both) return Run{t0 + s, t1, 2};
+    const int l = s ? lo1 : lo0, h = s ? hi1 : hi0;
+    if (h <= l) return Run{t1, t1, 1};
+    return Run{max(t0, l / kTile), min(t1, (h + kTile - 1) / kTile), 1};
+  };
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int n_all = kPrefix ? (int)a.n_prefix : (int)seq.n;
-  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)b * a.pm.max_pages;
-  // tiles of the CTA, then this split's run of them
-  const int lo = min(range[0], range[2]), hi = max(range[1], range[3]);
-  const int first = lo < hi ? lo / kTile : 0, last = lo < hi ? (hi + kTile - 1) / kTile : 0;
-  const int per = (last - first + t.splits - 1) / t.splits;
-  const int t0 = first + split * per, t1 = min(last, t0 + per);
-
-  // the tiles that a slot works on
-  auto run_of = [&](int s) -> Run {
-    if (!both) return Run{t0 + s, t1, 2};
-    return Run{max(t0, range[2 * s] / kTile), min(t1, (range[2 * s + 1] + kTile - 1) / kTile), 1};
-  };
 
   // The softmax threads hold a row's 128 scores: of the launch's 384 x 168
   // registers 2 x 128 x 200 go to them, 128 x 104 stay with the others.
@@ -474,7 +474,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         tc::mma_commit(&k_empty[stage]);
       };
       if (ok && run.first < run.last) {
-        ok = all(wait(&k_full[ks], kph, abort, a.wait_ns));
+        ok = all(wait(&q_full[both ? s : 0], 0, abort, a.wait_ns)) && all(wait(&k_full[ks], kph, abort, a.wait_ns));
         tc::fence_after_sync();
         if (ok && elected()) issue_s(ks);
         __syncwarp();
@@ -518,7 +518,40 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------- softmax: one row per thread ----------------
-    const bool active = (both ? warp : warp & 3) * 32 < nrows;
+    const int slot = warp >> 2, row = both ? threadIdx.x : (threadIdx.x & (kTile - 1));
+    const bool active = (both ? warp : warp & 3) * 32 < nrows, live = row < nrows;
+    const int tok = (row_base + row) / g, head = (row_base + row) % g;  // new token within its sequence
+    const int64_t my_out = (seq.first + tok) * a.Hq + j * g + head;     // row of out
+    if (active && (both || slot == 0)) {
+      // queries to shared memory, two rows at a time
+      const int64_t my_q = (seq.first + tok) * a.q_stride + (int64_t)(j * g + head) * kHeadDim;
+      const int c = lane & 15, x0 = row & (kTile - 32);
+      const uint32_t dst = tc::smem_u32(smem + Layout::kQ) + slot * kBuf + (c >> 3) * kHalf;
+#pragma unroll 1
+      for (int x = lane >> 4; x < 32; x += 2) {
+        const int64_t at = __shfl_sync(0xffffffffu, my_q, x);
+        const bool in = row - lane + x < nrows;  // rows behind the last one are zeros
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (in ? at + c * 8 : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (x0 + x) * 128 + (((c & 7) ^ (x & 7)) << 4)),
+                     "l"(src), "r"(in ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      async_fence();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[slot]);
+    }
+    pa::Span sp{0, INT32_MAX, 0};  // rows that are only padding see everything: no masks for their sake
+    if (live) {
+      if constexpr (kPrefix) {
+        const int64_t n = min((int64_t)max(a.n_tok[tok], 0), a.n_max);
+        sp = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
+      } else {
+        sp = pa::span_of(a, seq, b, tok, true);
+      }
+    }
+    // tiles within [all_lo, all_hi) are seen whole by every row of the warp
+    const int all_lo = __reduce_max_sync(0xffffffffu, sp.lo), all_hi = __reduce_min_sync(0xffffffffu, sp.hi);
     const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
     float m = -INFINITY, l = 0.f;
     int done = 0;  // tiles that this slot has been through
@@ -535,8 +568,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       tc::fence_after_sync();
       const int u0 = n * kTile;
       const uint4 there = valid_s[(n - t0) % kMaskRing];
-      const bool whole = sp.lo <= u0 && sp.hi >= u0 + kTile && (there.x & there.y & there.z & there.w) == ~0u;
-      const bool masked = __any_sync(0xffffffffu, !whole);
+      const bool masked = all_lo > u0 || all_hi < u0 + kTile || (there.x & there.y & there.z & there.w) != ~0u;
       // Scores that are more than a multiple of the products are formed first
       // and go back to tensor memory.  Loops over 32 columns stay rolled: a
       // row's 128 scores in registers meant spills and code that the
@@ -544,11 +576,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       auto form = [&] {
         const float d0 = (float)(sp.pos - u0);
         const uint32_t w[4] = {there.x, there.y, there.z, there.w};
-#pragma unroll 2
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           uint32_t v[32];
           tc::tmem_ld32(s_tmem + 32 * k, v);
-          tc::tmem_wait_ld();
+          tmem_arrived(v);
           const uint32_t in = k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3];
           const int lo = min(max(sp.lo - u0 - 32 * k, 0), 32), hi = min(max(sp.hi - u0 - 32 * k, 0), 32);
           // bit i: token i is seen
@@ -578,7 +610,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           uint32_t v[2][32];
           tc::tmem_ld32(s_tmem + 32 * k, v[0]);
           tc::tmem_ld32(s_tmem + 32 * k + 32, v[1]);
-          tc::tmem_wait_ld();
+          tmem_arrived(v[0]);
+          tmem_arrived(v[1]);
 #pragma unroll
           for (int i = 0; i < 32; i += 2)
 #pragma unroll
@@ -611,11 +644,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           const bool ok2 = wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
           if (!__all_sync(0xffffffffu, ok2)) break;
           tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tc::tmem_ld32(o_tmem + 32 * k, o);
-            tc::tmem_wait_ld();
+            tmem_arrived(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tmem_st32(o_tmem + 32 * k, o);
@@ -653,13 +686,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         // the next 32 columns are on their way while these are weighed
         uint32_t va[32], vb[32], vc[32], vd[32];
         tc::tmem_ld32(s_tmem, va);
-        tc::tmem_wait_ld();
+        tmem_arrived(va);
         tc::tmem_ld32(s_tmem + 32, vb);
         weigh(va, 0, raw);
-        tc::tmem_wait_ld();
+        tmem_arrived(vb);
         tc::tmem_ld32(s_tmem + 64, vc);
         weigh(vb, 1, raw);
-        tc::tmem_wait_ld();
+        tmem_arrived(vc);
         // P V may start on these 64 tokens
         tmem_wait_st();
         tc::fence_before_sync();
@@ -667,7 +700,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (lane == 0) tc::mbar_arrive(&p_half[slot]);
         tc::tmem_ld32(s_tmem + 96, vd);
         weigh(vc, 2, raw);
-        tc::tmem_wait_ld();
+        tmem_arrived(vd);
         weigh(vd, 3, raw);
       };
       if (kMode == kCapped && !formed)
@@ -697,12 +730,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (slot == 1 && active) {
         other[kTile * kTile + row] = m, other[kTile * kTile + kTile + row] = l;
         if (done > 0) {
-  #pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
             uint32_t o[32];
             tc::tmem_ld32(o_tmem + 32 * k, o);
-            tc::tmem_wait_ld();
-  #pragma unroll
+            tmem_arrived(o);
+#pragma unroll
             for (int i = 0; i < 32; ++i) other[(32 * k + i) * kTile + row] = __uint_as_float(o[i]);
           }
         }
@@ -718,36 +751,55 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         scale1 = m1 == -INFINITY ? 0.f : pa::ex2(m1 - top);
         l = l * scale0 + l1 * scale1, m = top;
       }
-      const int64_t out_row = (seq.first + tok) * a.Hq + j * a.g + head;
       const bool partial = t.part0 >= 0;
       const bool none = m == -INFINITY;  // nothing seen: O was never written, or means nothing
       const float inv = partial ? 1.f : none ? 0.f : 1.f / l;
-      const int64_t part_row = partial ? (t.part0 + split) * a.T * a.Hq + out_row : 0;
-      if (live && partial) a.part_ml[part_row] = make_float2(m, none ? 0.f : l);
+      const int64_t out_row = (partial ? (t.part0 + split) * a.T * a.Hq : 0) + my_out;
+      if (live && partial) a.part_ml[out_row] = make_float2(m, none ? 0.f : l);
       if (live && !partial && a.lse) a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * pa::kLn2;
-  #pragma unroll
+      // Rows leave through shared memory (the queries' place: this slot's MMAs
+      // are through with them), so that a row is written as whole lines: 256
+      // bytes of 32 rows at a time, 16-byte pieces swizzled by the row.
+      unsigned char* mine = smem + Layout::kQ + slot * kBuf + (warp & 3) * 8192;
+      unsigned char* dst = partial ? reinterpret_cast<unsigned char*>(a.part_o) : static_cast<unsigned char*>(a.out);
+      const int row_bytes = partial ? 512 : 256;
+      auto leave = [&](int at) {
+        __syncwarp();
+#pragma unroll 2
+        for (int x = lane >> 4; x < 32; x += 2) {
+          const int c = lane & 15;
+          const int64_t to = __shfl_sync(0xffffffffu, out_row, x);
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + x * 256 + ((c ^ (x & 15)) << 4));
+          if (row - lane + x < nrows) *reinterpret_cast<uint4*>(dst + to * row_bytes + at + c * 16) = v;
+        }
+        __syncwarp();
+      };
+      // one weight for the row's values: the sum, and in the other slot's favour
+      const float w0 = none ? 0.f : scale0 * inv, w1 = none ? 0.f : scale1 * inv;
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         uint32_t o[32];
         tc::tmem_ld32(o_tmem + 32 * k, o);
-        tc::tmem_wait_ld();
+        tmem_arrived(o);
         float x[32];
-  #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = scale0 > 0.f ? __uint_as_float(o[i]) * scale0 : 0.f;
-          if (!both && scale1 > 0.f) x[i] = fmaf(other[(32 * k + i) * kTile + row], scale1, x[i]);
-          x[i] = none ? 0.f : x[i] * inv;
-        }
-        if (live && partial) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + part_row * kHeadDim + 32 * k);
-  #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kHeadDim + 32 * k);
-  #pragma unroll
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = w0 > 0.f ? __uint_as_float(o[i]) * w0 : 0.f;
+        if (w1 > 0.f)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = fmaf(other[(32 * k + i) * kTile + row], w1, x[i]);
+        auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4*>(mine + lane * 256 + ((c ^ (lane & 15)) << 4)) = v; };
+        if (partial) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            put((k & 1) * 8 + i, make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
+                                            __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3])));
+        } else {
+#pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+            put(4 * k + i, make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                      pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7])));
         }
+        if (partial ? (k & 1) : k == 3) leave(partial ? (k >> 1) * 256 : 0);
       }
     }
   }
