@@ -136,10 +136,11 @@ __device__ void finish(const Args& a, const Item& it, const float* o_s, const fl
       const float4 x = reinterpret_cast<const float4*>(o_s)[i];
       o = make_float4(w[parts] * x.x, w[parts] * x.y, w[parts] * x.z, w[parts] * x.w);
     }
-#pragma unroll 8
+    const float4* part = reinterpret_cast<const float4*>(a.part_o) + row * Q + i % Q;
+#pragma unroll 4
     for (int p = 0; p < parts; ++p) {
-      if (w[p] == 0.f) continue;  // an empty part's values need not have been written
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (p * n_rows + row) * Q + i % Q);
+      float4 x = __ldcg(part + p * n_rows * Q);
+      if (w[p] == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // an empty part's values need not have been written
       o.x = fmaf(w[p], x.x, o.x), o.y = fmaf(w[p], x.y, o.y), o.z = fmaf(w[p], x.z, o.z), o.w = fmaf(w[p], x.w, o.w);
     }
     put4(static_cast<T*>(a.out) + row * kHeadDim + i % Q * 4, o);
@@ -348,7 +349,6 @@ rows_mma_kernel(const __grid_constant__ Args a) {
     const uint32_t u = (uint32_t)step * kStep + (lane & 15);
     return step < last && (int)u < hi ? table[u / P] : -1;
   };
-  uint32_t there[kStages];  // tokens of each stage that have a place in the pool
   auto issue = [&](int step, int page, int stage) -> uint32_t {
     const uint32_t u = (uint32_t)step * kStep + (lane & 15);
     const bool in = step < last && (int)u < hi;
@@ -377,21 +377,28 @@ rows_mma_kernel(const __grid_constant__ Args a) {
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
   const float cap = a.softcap * pa::kLog2e;
-  int page = page_of(first + warp);
-#pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    const int step = first + warp + s * kMmaWarps, next = page_of(step + kMmaWarps);
-    there[s] = issue(step, page, s);
+  // The loops over steps stay rolled: a block runs through few of them, and
+  // fetching unrolled code for the first time took longer than running it.
+  // Bits 16 s ..: which tokens of the step issued s steps ago have a place in
+  // the pool.
+  uint64_t there_of = 0;
+  int page = page_of(first + warp), ahead = first + warp, slot = 0;
+  auto issue_next = [&] {
+    const int next = page_of(ahead + kMmaWarps);
+    there_of = there_of << 16 | issue(ahead, page, slot);
     page = next;
-  }
-  for (int step0 = first + warp; step0 < last; step0 += kStages * kMmaWarps) {
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) {
-      const int step = step0 + s * kMmaWarps;
-      if (step >= last) break;
+    ahead += kMmaWarps;
+    if (++slot == kStages) slot = 0;
+  };
+#pragma unroll 1
+  for (int s = 0; s < kStages; ++s) issue_next();
+  {
+#pragma unroll 1
+    for (int step = first + warp; step < last; step += kMmaWarps) {
+      const uint32_t there = (uint32_t)(there_of >> (16 * (kStages - 1))) & 0xffffu;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();
-      const uint32_t kb = my_ring + s * 2 * kStepBytes, vb = kb + kStepBytes;
+      const uint32_t kb = my_ring + slot * 2 * kStepBytes, vb = kb + kStepBytes;
       float z[2][4] = {};
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
@@ -404,7 +411,7 @@ rows_mma_kernel(const __grid_constant__ Args a) {
       }
       const int u0 = step * kStep + (lane & 3) * 2;  // this thread's tokens: u0, u0 + 1, u0 + 8, u0 + 9
       float top[2] = {-INFINITY, -INFINITY};
-      const bool whole = there[s] == 0xffffu && sp[0].lo <= step * kStep && sp[1].lo <= step * kStep &&
+      const bool whole = there == 0xffffu && sp[0].lo <= step * kStep && sp[1].lo <= step * kStep &&
                          sp[0].hi >= (step + 1) * kStep && sp[1].hi >= (step + 1) * kStep;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -416,7 +423,7 @@ rows_mma_kernel(const __grid_constant__ Args a) {
             if (cap > 0.f) x = pa::capped(x, cap);
             x = fmaf(-slope[h], fabsf((float)(sp[h].pos - u)), x);
           }
-          if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there[s] >> (u & 15) & 1u))) x = -INFINITY;
+          if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there >> (u & 15) & 1u))) x = -INFINITY;
           z[n][e] = x;
           top[h] = fmaxf(top[h], x);
         }
@@ -455,9 +462,7 @@ rows_mma_kernel(const __grid_constant__ Args a) {
         mma16816(acc[2 * d + 1], pf, b[2], b[3]);
       }
       __syncwarp();
-      const int ahead = step + kStages * kMmaWarps, next = page_of(ahead + kMmaWarps);
-      there[s] = issue(ahead, page, s);
-      page = next;
+      issue_next();
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");

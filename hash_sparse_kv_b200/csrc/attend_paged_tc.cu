@@ -586,14 +586,16 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           // bit i: token i is seen
           const uint32_t see = masked ? in & (uint32_t)((1ull << hi) - 1) & ~(uint32_t)((1ull << lo) - 1) : ~0u;
           const float d = d0 - (float)(32 * k);
+          if (kMode != kPlain && cap > 0.f) {
+            const float size = kMode == kBiased ? cap : 1.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(pa::capped(__uint_as_float(v[i]) * to_cap, size));
+          }
+          const float by = cap > 0.f ? 1.f : a.scale * pa::kLog2e;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float z = __uint_as_float(v[i]);
-            if (kMode == kCapped) z = pa::capped(z * to_cap, 1.f);
-            if (kMode == kBiased) {
-              z = cap > 0.f ? pa::capped(z * to_cap, cap) : z * (a.scale * pa::kLog2e);
-              z = fmaf(-slope, fabsf(d - (float)i), z);
-            }
+            if (kMode == kBiased) z = fmaf(-slope, fabsf(d - (float)i), z * by);
             v[i] = see >> i & 1u ? __float_as_uint(z) : 0xff800000u;  // -inf
           }
           tmem_st32(s_tmem + 32 * k, v);
