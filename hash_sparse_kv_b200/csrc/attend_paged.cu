@@ -6,8 +6,8 @@
 // heads a token share its keys) and one run of their cache positions, reads
 // that run once, and keeps the softmax's running maximum and sum and the
 // weighted values in registers (fp32).  Where few blocks would be left, the
-// positions are split over several blocks; each stores its partial and the
-// last to finish (a ticket per item) joins them.
+// positions are split over several blocks and a second launch joins their
+// partial results.
 #include <cstdio>
 
 #include "attend_paged.cuh"
@@ -20,7 +20,6 @@ using pa::Args;
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
 constexpr int kTile = 32;
-constexpr int kMaxParts = 224;  // parts that a row is joined from, at most
 
 __device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
@@ -70,80 +69,26 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Item& it, int r)
 }
 
 // The block's result: maximum, sum and weighted values of its rows, in shared
-// memory (o_s [kRows][kHeadDim], m_s and l_s [kRows]).  `w_s` is shared memory for
-// kRows * parts weights.  Every thread of the block comes here after a barrier.
+// memory (o_s [kRows][kHeadDim], m_s and l_s [kRows]).  Every thread of the block
+// comes here after a barrier.
 template <typename T, bool kPrefix>
-__device__ void finish(const Args& a, const Item& it, const float* o_s, const float* m_s, const float* l_s, float* w_s,
-                       int* last_s) {
+__device__ void finish(const Args& a, const Item& it, const float* o_s, const float* m_s, const float* l_s) {
   constexpr int Q = kHeadDim / 4;  // float4 pieces of a row
-  const int tid = threadIdx.x, nthr = blockDim.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t n_rows = a.T * a.Hq;
-  const int mine = kPrefix ? blockIdx.z : a.prefix_parts + blockIdx.z;
-  const bool alone = !kPrefix && a.own_parts == 1;  // this block's partial need not go through memory
-  if (!alone) {
-    for (int i = tid; i < it.nrows * Q; i += nthr) {
-      const int64_t row = mine * n_rows + out_row(a, it, i / Q);
-      reinterpret_cast<float4*>(a.part_o)[row * Q + i % Q] = reinterpret_cast<const float4*>(o_s)[i];
-      if (i % Q == 0) a.part_ml[row] = make_float2(m_s[i / Q], l_s[i / Q]);
-    }
-    if constexpr (kPrefix) return;
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t* t = a.tickets + (int64_t)blockIdx.x * a.Hkv + it.j;
-      *last_s = atomicAdd(t, 1u) == (uint32_t)a.own_parts - 1;
-      if (*last_s) *t = 0;  // ready for the next call
-    }
-    __syncthreads();
-    if (!*last_s) return;
-    __threadfence();
-  }
-  const int parts = alone ? a.prefix_parts : a.prefix_parts + a.own_parts;
-  // a warp per row: the parts' weights, this block's own (if it is not among
-  // them) last, and the log-sum-exp
-  for (int r = warp; r < it.nrows; r += nthr / 32) {
-    const int64_t row = out_row(a, it, r);
-    float M = alone ? m_s[r] : -INFINITY;
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(&a.part_ml[p * n_rows + row].x));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-      const float2 ml = __ldcg(&a.part_ml[p * n_rows + row]);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      w_s[r * (parts + 1) + p] = w;
-      L = fmaf(w, ml.y, L);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float own = alone && m_s[r] != -INFINITY ? exp2f(m_s[r] - M) : 0.f;
-    if (alone) L = fmaf(own, l_s[r], L);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    __syncwarp();
-    for (int p = lane; p < parts; p += 32) w_s[r * (parts + 1) + p] *= inv;
-    if (lane == 0) {
-      w_s[r * (parts + 1) + parts] = own * inv;
-      if (a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < it.nrows * Q; i += nthr) {
+  const int parts = a.prefix_parts + a.own_parts;
+  for (int i = threadIdx.x; i < it.nrows * Q; i += blockDim.x) {
     const int r = i / Q;
-    const int64_t row = out_row(a, it, r);
-    const float* w = w_s + r * (parts + 1);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (w[parts] > 0.f) {
-      const float4 x = reinterpret_cast<const float4*>(o_s)[i];
-      o = make_float4(w[parts] * x.x, w[parts] * x.y, w[parts] * x.z, w[parts] * x.w);
+    int64_t row = out_row(a, it, r);
+    float4 x = reinterpret_cast<const float4*>(o_s)[i];
+    if (parts > 1) {
+      row += (kPrefix ? blockIdx.z : a.prefix_parts + blockIdx.z) * a.T * a.Hq;
+      reinterpret_cast<float4*>(a.part_o)[row * Q + i % Q] = x;
+      if (i % Q == 0) a.part_ml[row] = make_float2(m_s[r], l_s[r]);
+    } else {
+      const float inv = l_s[r] > 0.f ? 1.f / l_s[r] : 0.f;
+      x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      put4(static_cast<T*>(a.out) + row * kHeadDim + i % Q * 4, x);
+      if (i % Q == 0 && a.lse) a.lse[row] = l_s[r] > 0.f ? (m_s[r] + log2f(l_s[r])) * pa::kLn2 : -INFINITY;
     }
-    const float4* part = reinterpret_cast<const float4*>(a.part_o) + row * Q + i % Q;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      float4 x = __ldcg(part + p * n_rows * Q);
-      if (w[p] == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // an empty part's values need not have been written
-      o.x = fmaf(w[p], x.x, o.x), o.y = fmaf(w[p], x.y, o.y), o.z = fmaf(w[p], x.z, o.z), o.w = fmaf(w[p], x.w, o.w);
-    }
-    put4(static_cast<T*>(a.out) + row * kHeadDim + i % Q * 4, o);
   }
 }
 
@@ -153,11 +98,10 @@ rows_simt_kernel(const __grid_constant__ Args a) {
   constexpr int D = kHeadDim, KP = D + 1;
   __shared__ __align__(16) float q_s[kRows][D];  // the block's result in the end
   __shared__ __align__(16) float k_s[kTile][KP];
-  __shared__ __align__(16) float v_s[kTile][D];  // the joined parts' weights in the end
+  __shared__ __align__(16) float v_s[kTile][D];
   __shared__ float p_s[kRows][kTile];
   __shared__ float m_s[kRows], l_s[kRows], f_s[kRows];
   __shared__ int64_t row_s[kTile];
-  __shared__ int last_s;
   const int tid = threadIdx.x;
   Item it;
   if (!item_of<kPrefix>(a, it)) return;
@@ -253,8 +197,7 @@ rows_simt_kernel(const __grid_constant__ Args a) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) q_s[ar0 + k][col] = acc[k];
   __syncthreads();
-  static_assert(kRows * (kMaxParts + 1) <= kTile * D, "weights must fit v_s");
-  finish<T, kPrefix>(a, it, q_s[0], m_s, l_s, v_s[0], &last_s);
+  finish<T, kPrefix>(a, it, q_s[0], m_s, l_s);
 }
 
 // ---- bf16: the same on the tensor cores of one warp --------------------------
@@ -302,7 +245,7 @@ rows_mma_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) unsigned char ring[];  // [warp][stage][K step, V step]; the parts in the end
   __shared__ __align__(16) __nv_bfloat16 q_s[kRows][kQPitch];
   __shared__ float m_s[kMmaWarps][kRows], l_s[kMmaWarps][kRows];
-  __shared__ int span_s[2], last_s;
+  __shared__ int span_s[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Item it;
   if (!item_of<false>(a, it)) return;
@@ -502,15 +445,88 @@ rows_mma_kernel(const __grid_constant__ Args a) {
     o_w[i] = x;
   }
   __syncthreads();
-  static_assert(kRows * (kMaxParts + 1) * sizeof(float) + kMmaWarps * kRows * D * sizeof(float) <= kMmaSmem, "weights");
-  finish<__nv_bfloat16, false>(a, it, o_w, mm, ll, o_w + kMmaWarps * kRows * D, &last_s);
+  finish<__nv_bfloat16, false>(a, it, o_w, mm, ll);
+  // launched while the prefix's kernel may still run: whatever waits for this
+  // grid waits for that one too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Splits that fill the GPU about twice over, each with at least four tiles.
-int splits_for(int64_t items, int64_t tokens, int tile) {
-  const int64_t want = ceil_div(2 * (int64_t)sm_count(), items < 1 ? 1 : items);
-  const int64_t most = ceil_div(tokens, 4 * (int64_t)tile);
-  const int64_t s = want < most ? want : most;
+// Joins the parts of every row: out = sum_p 2^(m_p - M) o_p / L, with M the
+// largest m_p and L = sum_p 2^(m_p - M) l_p.  One warp per row, four columns a
+// lane; the parts' loads are independent of one another.
+template <typename T>
+__global__ void __launch_bounds__(128)
+join_parts_kernel(const __grid_constant__ Args a) {
+  constexpr int Q = kHeadDim / 4, kAhead = 4;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n_rows = a.T * a.Hq;
+  const int lane = threadIdx.x & 31, parts = a.prefix_parts + a.own_parts;
+  if (row >= n_rows) return;
+  if (a.cu) {
+    const int64_t t = row / a.Hq;
+    const pa::Seq s = pa::seq_of(a, pa::find_seq(a.cu, a.B, t), false);
+    if (t < s.first || t >= s.first + s.n_new) return;  // behind the last sequence
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float2* ml = a.part_ml + row;
+  const float4* part = reinterpret_cast<const float4*>(a.part_o) + row * Q + lane;
+  float M = -INFINITY;
+  for (int p = lane; p < parts; p += 32) M = fmaxf(M, ml[p * n_rows].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    // lane p holds the weight of part p0 + p; an empty part's values need not
+    // have been written
+    const float2 mine = p0 + lane < parts ? ml[(p0 + lane) * n_rows] : make_float2(-INFINITY, 0.f);
+    const float w = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
+    L = fmaf(w, mine.y, L);
+    const int n = min(32, parts - p0);
+    for (int p = 0; p < n; p += kAhead) {
+      float4 x[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e)
+        x[e] = p + e < n ? part[(p0 + p + e) * n_rows * Q] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const float v = __shfl_sync(0xffffffffu, w, (p + e) & 31);
+        if (v > 0.f && p + e < n)
+          o.x = fmaf(v, x[e].x, o.x), o.y = fmaf(v, x[e].y, o.y), o.z = fmaf(v, x[e].z, o.z), o.w = fmaf(v, x[e].w, o.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  put4(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (lane == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
+}
+
+// Launches a kernel that may be scheduled while the one before it on the stream
+// still runs (it waits for that one itself).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
+// Runs of positions that an item's blocks take: few items are cut until two
+// blocks per SM are there, down to 128 tokens; many items only into runs of at
+// least 2048 tokens, eight blocks per SM, so that the last ones to run are
+// short (64 sequences of up to 8192 tokens: 306 us whole, 277 us in runs of
+// 2730).
+int splits_for(int64_t items, int64_t tokens) {
+  const int64_t sms = sm_count();
+  auto cut = [&](int64_t per_sm, int64_t least) {
+    const int64_t want = ceil_div(per_sm * sms, items < 1 ? 1 : items), most = ceil_div(tokens, least);
+    return want < most ? want : most;
+  };
+  const int64_t few = cut(2, 128), many = cut(8, 2048), s = few > many ? few : many;
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
@@ -521,58 +537,67 @@ struct Plan {
   bool tc_prefix = false;  // it takes the shared prefix
   int64_t own_items = 0;
   int prefix_parts = 0, own_parts = 1;
-  size_t ml = 0, o = 0, total = 0;  // byte offsets of part_ml and part_o, and the size
+  int parts = 0;          // a row's partial results, 0 when its block finishes it
+  size_t o = 0, total = 0;  // byte offset of part_o behind part_ml, and the size
 };
 
 Plan plan(const PagedAttend& p) {
   Plan r;
   const int g = p.Hq / p.Hkv, tpt = kRows / g;
   const bool bf16 = p.dtype == HKV_BF16;
-  int64_t parts = 0;
   // a sequence's new tokens fill more than the 16 rows of one block: 128-row tiles
   r.tc = bf16 && p.cu_q_rows && (int64_t)p.max_q * g > kRows;
   if (r.tc) {
     r.own_parts = tc_splits(p, false);
   } else {
     r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt);
-    r.own_parts = splits_for(r.own_items * p.Hkv, p.n_max, kTile);
+    r.own_parts = splits_for(r.own_items * p.Hkv, p.n_max);
     r.tc_prefix = bf16 && p.n_prefix > 0;
     if (r.tc_prefix)
       r.prefix_parts = tc_splits(p, true);
     else if (p.n_prefix > 0)
-      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix, kTile);
+      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix);
   }
-  parts = r.prefix_parts + (r.own_parts > 1 ? r.own_parts : 0);
-  r.ml = align_up(sizeof(uint32_t) * r.own_items * p.Hkv, 256);
-  r.o = r.ml + align_up(sizeof(float2) * parts * p.T * p.Hq, 256);
-  r.total = parts ? r.o + sizeof(float) * kHeadDim * parts * p.T * p.Hq : 0;
+  r.parts = r.prefix_parts > 0 || r.own_parts > 1 ? r.prefix_parts + r.own_parts : 0;
+  r.o = align_up(sizeof(float2) * r.parts * p.T * p.Hq, 256);
+  r.total = r.parts ? r.o + sizeof(float) * kHeadDim * r.parts * p.T * p.Hq : 0;
   return r;
 }
 
 template <typename T>
 int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
-  if (pl.tc) return launch_attend_tc(p, a, false, pl.own_parts, pl.own_parts > 1 ? 0 : -1, st);
-  if (pl.tc_prefix) {
-    const int rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
-    if (rc != HKV_OK) return rc;
-  } else if (pl.prefix_parts > 0) {
-    if constexpr (sizeof(T) == 4) {
-      const dim3 grid((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts);
-      rows_simt_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
-      const int rc = cuda_check(cudaGetLastError(), "prefix attention launch");
+  int rc = HKV_OK;
+  if (pl.tc) {
+    rc = launch_attend_tc(p, a, false, pl.own_parts, pl.parts ? 0 : -1, st);
+  } else {
+    if (pl.prefix_parts > 0) {
+      if constexpr (sizeof(T) == 4) {
+        rows_simt_kernel<T, true><<<dim3((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts), kThreads, 0, st>>>(a);
+        rc = cuda_check(cudaGetLastError(), "prefix attention launch");
+      } else {
+        rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
+      }
       if (rc != HKV_OK) return rc;
     }
+    const dim3 grid((unsigned)pl.own_items, p.Hkv, pl.own_parts);
+    if constexpr (sizeof(T) == 2) {
+      auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmaSmem);
+      if (e == cudaSuccess) {
+        if (pl.prefix_parts > 0)  // beside the prefix's kernel, which it does not depend on
+          e = launch_after(kernel, grid, kMmaThreads, kMmaSmem, st, a);
+        else
+          kernel<<<grid, kMmaThreads, kMmaSmem, st>>>(a), e = cudaGetLastError();
+      }
+      rc = cuda_check(e, "paged attention launch");
+    } else {
+      rows_simt_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+      rc = cuda_check(cudaGetLastError(), "paged attention launch");
+    }
   }
-  const dim3 grid((unsigned)pl.own_items, p.Hkv, pl.own_parts);
-  if constexpr (sizeof(T) == 2) {
-    auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmaSmem);
-    if (e != cudaSuccess) return cuda_check(e, "paged attention smem attribute");
-    kernel<<<grid, kMmaThreads, kMmaSmem, st>>>(a);
-  } else {
-    rows_simt_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
-  }
-  return cuda_check(cudaGetLastError(), "paged attention launch");
+  if (rc != HKV_OK || pl.parts == 0) return rc;
+  return cuda_check(launch_after(join_parts_kernel<T>, dim3((unsigned)ceil_div(a.T * a.Hq, 4)), 128, 0, st, a),
+                    "attention join launch");
 }
 
 }  // namespace
@@ -593,8 +618,7 @@ int launch_attend_paged(const PagedAttend& p, void* ws, size_t ws_bytes, cudaStr
   a.wait_ns = wait_limit_ns();
   a.prefix_parts = pl.prefix_parts, a.own_parts = pl.own_parts;
   unsigned char* w = static_cast<unsigned char*>(ws);
-  a.tickets = reinterpret_cast<uint32_t*>(w);
-  a.part_ml = reinterpret_cast<float2*>(w + pl.ml);
+  a.part_ml = reinterpret_cast<float2*>(w);
   a.part_o = reinterpret_cast<float*>(w + pl.o);
   return p.dtype == HKV_BF16 ? run<__nv_bfloat16>(p, pl, a, st) : run<float>(p, pl, a, st);
 }

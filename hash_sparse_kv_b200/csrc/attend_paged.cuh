@@ -43,7 +43,6 @@ struct Args {
   // partials of rows whose positions are split: [part][T * Hq] rows
   float* part_o;
   float2* part_ml;            // running maximum (log2 units) and sum
-  uint32_t* tickets;          // zero before and after every call
   int prefix_parts, own_parts;
   int32_t* status;
   uint64_t wait_ns;

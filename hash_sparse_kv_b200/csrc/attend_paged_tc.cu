@@ -365,6 +365,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tc::mbar_init_fence();
   }
   if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes next may take the SMs that are free
   // What a slot's rows see together, a bound rather than the exact union:
   // positions grow with the rows.  Every warp works it out for itself.
   const int g = a.g, row_base = (int)r0;  // r0 + 255 < T * g < 2^31
@@ -815,34 +816,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   }
 }
 
-// Joins the splits of a prompt's rows: one warp per row, four columns per lane.
-__global__ void __launch_bounds__(256)
-join_parts_kernel(const __grid_constant__ Args a, int parts) {
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= a.T * a.Hq) return;
-  const int64_t t = row / a.Hq, n_rows = a.T * a.Hq;
-  const int b = pa::find_seq(a.cu, a.B, t);
-  const pa::Seq s = pa::seq_of(a, b, false);
-  if (t < s.first || t >= s.first + s.n_new) return;  // behind the last sequence
-  float M = -INFINITY;
-  for (int p = 0; p < parts; ++p) M = fmaxf(M, a.part_ml[p * n_rows + row].x);
-  float L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < parts; ++p) {
-    const float2 ml = a.part_ml[p * n_rows + row];
-    if (ml.x == -INFINITY) continue;
-    const float w = exp2f(ml.x - M);
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (p * n_rows + row) * kHeadDim + lane * 4);
-    L = fmaf(w, ml.y, L);
-    o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
-  }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHeadDim + lane * 4) =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  if (lane == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
-}
-
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -883,11 +856,10 @@ int64_t tc_tiles(const PagedAttend& p, bool prefix) {
 }
 
 // One wave of CTAs where the rows alone leave SMs idle, each with at least
-// four tiles of positions (a CTA's prologue and the joining of parts cost
-// about as much as two tiles).
+// two tiles of positions (with at most 128 rows, one for each slot).
 int tc_splits(const PagedAttend& p, bool prefix) {
   const int64_t ctas = tc_tiles(p, prefix) * p.Hkv, sms = sm_count();
-  const int64_t most = ceil_div(prefix ? p.n_prefix : p.n_max, 4 * kTile);
+  const int64_t most = ceil_div(prefix ? p.n_prefix : p.n_max, 2 * kTile);
   int64_t s = sms / (ctas < 1 ? 1 : ctas);
   s = s < most ? s : most;
   return (int)(s < 1 ? 1 : s);
@@ -916,10 +888,7 @@ int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int s
   const int64_t grid = (int64_t)t.tiles * splits * p.Hkv;
   if (grid > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "too many row tiles (%lld)", (long long)grid);
   kernel<<<(unsigned)grid, kThreads, kSmem, st>>>(kmap, vmap, t);
-  int rc = cuda_check(cudaGetLastError(), "attention launch");
-  if (rc != HKV_OK || prefix || part0 < 0) return rc;
-  join_parts_kernel<<<(unsigned)ceil_div(a.T * a.Hq, 8), 256, 0, st>>>(a, splits);
-  return cuda_check(cudaGetLastError(), "attention join launch");
+  return cuda_check(cudaGetLastError(), "attention launch");
 }
 
 }  // namespace hkv
