@@ -683,6 +683,9 @@ def hkv_decode_step_normw(q, k_codes, norms, K, V, n_tokens: int, n_sink: int, n
                                     _stream(stream)))
 
 
+_SCALE = 1.0 / math.sqrt(128)
+
+
 class RopeParams:
     """Rotary positions (the C struct hkv_rope).  inv_freq [pairs] fp32 on the device; pair i is the elements
     (i, i + pairs) of a head, or (2 i, 2 i + 1) when interleaved.  sections: how many pairs each position axis turns,
@@ -708,23 +711,57 @@ class RopeParams:
         self.c = hkv_rope(pairs, int(interleaved), n_axes, 0, inv_freq.data_ptr(), (ctypes.c_uint8 * 64)(*axis))
 
 
-def _here(*tensors) -> None:
-    """Every tensor is on the current device, on whose stream the call is issued."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+def _here(t: torch.Tensor, name: str, dev: int) -> None:
+    """t is on the current device, on whose stream the call is issued."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
 
 
-def _need_rows(t: torch.Tensor, name: str, dtype, shape) -> None:
-    """[T, heads, 128] with dense heads; the rows may be further apart (e.g. a slice of a fused projection)."""
-    _need(t, name, dtype, shape=shape, contiguous=False)
-    if t.numel() and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != 128)):
+# The paged serving calls take a dozen tensors a call and a decode step is a few
+# microseconds, so their checks look at each tensor once and only a tensor that
+# fails goes through _need for the message.
+def _ck(dev: int, t: torch.Tensor, name: str, dtype, shape) -> None:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _need(t, name, dtype, shape=shape)
+        _here(t, name, dev)
+
+
+def _ck_rows(dev: int, t: torch.Tensor, name: str, dtype, shape) -> int:
+    """[T, heads, 128] with dense heads; the rows may be further apart (e.g. a slice of a fused projection).
+    Returns their distance."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _need(t, name, dtype, shape=shape, contiguous=False)
+        _here(t, name, dev)
+    rows, heads, one = t.stride()
+    if t.numel() and (one != 1 or (shape[1] > 1 and heads != 128)):
         raise ValueError(f"{name} must have dense heads")
+    return rows if shape[0] > 1 else max(rows, shape[1] * 128)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * 128)
+def _ck_ws(dev: int, ws: Optional[torch.Tensor], status: Optional[torch.Tensor]):
+    """(pointer, bytes) of the workspace and the pointer of the status word."""
+    if status is not None:
+        _ck(dev, status, "status", torch.int32, (1,))
+    if ws is None:
+        return None, 0, None if status is None else status.data_ptr()
+    _here(ws, "ws", dev)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), None if status is None else status.data_ptr()
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _row_dtype(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _dtype_code(t)
 
 
 def hkv_append_paged_workspace_bytes(h: Optional[HashParams], T: int, Hkv: int) -> int:
@@ -734,7 +771,7 @@ def hkv_append_paged_workspace_bytes(h: Optional[HashParams], T: int, Hkv: int) 
 def append_workspace(h: Optional[HashParams], T: int, Hkv: int, device=None) -> Optional[torch.Tensor]:
     """The workspace of hkv_append_paged, or None when it needs none (bf16 LSH, SIGN, no hash)."""
     n = hkv_append_paged_workspace_bytes(h, T, Hkv)
-    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return _scratch(n, device)
 
 
 def hkv_append_paged(h: Optional[HashParams], k_new, v_new, K_pool, V_pool, page_table, cu_new, n_past, codes_pool=None,
@@ -744,69 +781,75 @@ def hkv_append_paged(h: Optional[HashParams], k_new, v_new, K_pool, V_pool, page
     k_new, v_new [T, Hkv, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; page_table
     [B, max_pages], cu_new [B + 1], n_past [B] int32; codes_pool [num_pages, Hkv, page_size, W] with a hash; positions
     int32 [n_axes, T] (default: the position in the cache); q, q_out [T, Hq, 128] (q_out may be q)."""
-    num_pages, Hkv, page_size, d = K_pool.shape
-    T, B = k_new.shape[0], page_table.shape[0]
-    _need(k_new, "k_new", (torch.bfloat16, torch.float32), contiguous=False)
-    dt = k_new.dtype
-    _need_rows(k_new, "k_new", dt, (T, Hkv, 128))
-    _need_rows(v_new, "v_new", dt, (T, Hkv, 128))
-    _need(K_pool, "K_pool", dt, shape=(num_pages, Hkv, page_size, 128))
-    _need(V_pool, "V_pool", dt, shape=(num_pages, Hkv, page_size, 128))
-    _need(page_table, "page_table", torch.int32)
+    num_pages, Hkv, page_size, _ = K_pool.shape
+    T, dt, code = k_new.shape[0], k_new.dtype, _row_dtype(k_new, "k_new")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _need(cu_new, "cu_new", torch.int32, shape=(B + 1,))
-    _need(n_past, "n_past", torch.int32, shape=(B,))
-    if h is None and (codes_pool is not None or norms_pool is not None):
-        raise ValueError("codes_pool and norms_pool need a hash")
-    if h is not None:
+    B, max_pages = page_table.shape
+    dev = torch.cuda.current_device()
+    rows = (T, Hkv, 128)
+    k_stride, v_stride = _ck_rows(dev, k_new, "k_new", dt, rows), _ck_rows(dev, v_new, "v_new", dt, rows)
+    pool = (num_pages, Hkv, page_size, 128)
+    _ck(dev, K_pool, "K_pool", dt, pool)
+    _ck(dev, V_pool, "V_pool", dt, pool)
+    _ck(dev, page_table, "page_table", torch.int32, (B, max_pages))
+    _ck(dev, cu_new, "cu_new", torch.int32, (B + 1,))
+    _ck(dev, n_past, "n_past", torch.int32, (B,))
+    if h is None:
+        if codes_pool is not None or norms_pool is not None:
+            raise ValueError("codes_pool and norms_pool need a hash")
+    else:
         if codes_pool is None:
             raise ValueError("a hash needs codes_pool")
-        _need(codes_pool, "codes_pool", _U32, shape=(num_pages, Hkv, page_size, h.words))
+        _ck(dev, codes_pool, "codes_pool", codes_pool.dtype if codes_pool.dtype in _U32 else torch.int32,
+            (num_pages, Hkv, page_size, h.words))
     if norms_pool is not None:
-        _need(norms_pool, "norms_pool", (torch.float16, torch.int16), shape=(num_pages, Hkv, page_size))
+        _ck(dev, norms_pool, "norms_pool", torch.int16 if norms_pool.dtype is torch.int16 else torch.float16,
+            (num_pages, Hkv, page_size))
     if positions is not None:
-        _need(positions, "positions", torch.int32, shape=(1 if rope is None else rope.n_axes, T))
-    Hq = 0
+        _ck(dev, positions, "positions", torch.int32, (1 if rope is None else rope.n_axes, T))
+    if rope is not None:
+        _here(rope.inv_freq, "rope inv_freq", dev)
+    Hq = q_stride = qo_stride = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         Hq = q.shape[1]
-        _need_rows(q, "q", dt, (T, Hq, 128))
-        _need_rows(q_out, "q_out", dt, (T, Hq, 128))
-    _here(k_new, v_new, K_pool, V_pool, page_table, cu_new, n_past, codes_pool, norms_pool, positions, q, q_out, ws, status,
-          None if rope is None else rope.inv_freq)
+        q_stride, qo_stride = _ck_rows(dev, q, "q", dt, (T, Hq, 128)), _ck_rows(dev, q_out, "q_out", dt, (T, Hq, 128))
+    ws_ptr, ws_bytes, status_ptr = _ck_ws(dev, ws, status)
     _ok(lib().hkv_append_paged(
-        None if h is None else ctypes.byref(h.c), _dtype_code(k_new), None if rope is None else ctypes.byref(rope.c), B, T,
-        Hq, Hkv, _ptr(q), 0 if q is None else _row_stride(q), _ptr(q_out), 0 if q is None else _row_stride(q_out),
-        _ptr(k_new), _row_stride(k_new), _ptr(v_new), _row_stride(v_new), _ptr(cu_new), _ptr(n_past), _ptr(positions),
-        _ptr(K_pool), _ptr(V_pool), _ptr(codes_pool), _ptr(norms_pool), _ptr(page_table), page_table.shape[1], num_pages,
-        page_size, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+        None if h is None else ctypes.byref(h.c), code, None if rope is None else ctypes.byref(rope.c), B, T, Hq, Hkv,
+        _at(q), q_stride, _at(q_out), qo_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride,
+        cu_new.data_ptr(), n_past.data_ptr(), _at(positions), K_pool.data_ptr(), V_pool.data_ptr(), _at(codes_pool),
+        _at(norms_pool), page_table.data_ptr(), max_pages, num_pages, page_size, ws_ptr, ws_bytes, status_ptr,
+        _raw_stream(stream, dev)))
 
 
-def _score(softcap, window, slopes, prefix_len, q_first, B, T, Hq) -> hkv_score:
+def _score(dev, softcap, window, slopes, prefix_len, q_first, B, T, Hq):
+    """The C struct by reference, or None for plain causal attention."""
     if slopes is not None:
-        _need(slopes, "slopes", torch.float32, shape=(Hq,))
+        _ck(dev, slopes, "slopes", torch.float32, (Hq,))
     if prefix_len is not None:
-        _need(prefix_len, "prefix_len", torch.int32, shape=(B,))
+        _ck(dev, prefix_len, "prefix_len", torch.int32, (B,))
     if q_first is not None:
-        _need(q_first, "q_first", torch.int32, shape=(T,))
-    return hkv_score(float(softcap), int(window), *(None if t is None else t.data_ptr()
-                                                    for t in (slopes, prefix_len, q_first)))
+        _ck(dev, q_first, "q_first", torch.int32, (T,))
+    if not softcap and not window and slopes is None and prefix_len is None and q_first is None:
+        return None
+    return ctypes.byref(hkv_score(softcap, window, _at(slopes), _at(prefix_len), _at(q_first)))
 
 
 def hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, dtype: int) -> int:
     return lib().hkv_prefill_workspace_bytes(B, T, Hq, Hkv, dtype, max_q, n_tokens_max)
 
 
-def _zeroed(n: int, device) -> Optional[torch.Tensor]:
-    return None if n == 0 else torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+def _scratch(n: int, device) -> Optional[torch.Tensor]:
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
 def prefill_workspace(B, Hq, Hkv, T, max_q, n_tokens_max, dtype=torch.bfloat16, device=None) -> Optional[torch.Tensor]:
-    """A zero-filled workspace for hkv_prefill_attend_paged, or None when this shape needs none."""
+    """The workspace of hkv_prefill_attend_paged, or None when this shape needs none."""
     code = _dtype_code(torch.empty(0, dtype=dtype))
-    return _zeroed(hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, code), device)
+    return _scratch(hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, code), device)
 
 
 def hkv_prefill_attend_paged(q, K_pool, V_pool, page_table, cu_q, n_tokens_b, max_q: int, n_tokens_max: int, out, lse=None,
@@ -816,28 +859,30 @@ def hkv_prefill_attend_paged(q, K_pool, V_pool, page_table, cu_q, n_tokens_b, ma
     q [T, Hq, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; page_table [B, max_pages],
     cu_q [B + 1], n_tokens_b [B] int32; out [T, Hq, 128] in q's dtype; lse [T, Hq] fp32.  softcap, slopes [Hq], window,
     prefix_len [B] and q_first [T] shape the scores and the mask (hkv_score in the header)."""
-    T, Hq, d = q.shape
+    T, Hq, _ = q.shape
     num_pages, Hkv, page_size, _ = K_pool.shape
-    B = page_table.shape[0]
-    _need(q, "q", (torch.bfloat16, torch.float32), contiguous=False)
-    _need_rows(q, "q", q.dtype, (T, Hq, 128))
-    _need(K_pool, "K_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
-    _need(V_pool, "V_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
-    _need(page_table, "page_table", torch.int32)
+    dt, code = q.dtype, _row_dtype(q, "q")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _need(cu_q, "cu_q", torch.int32, shape=(B + 1,))
-    _need(n_tokens_b, "n_tokens_b", torch.int32, shape=(B,))
-    _need(out, "out", q.dtype, shape=(T, Hq, 128))
+    B, max_pages = page_table.shape
+    dev = torch.cuda.current_device()
+    pool = (num_pages, Hkv, page_size, 128)
+    q_stride = _ck_rows(dev, q, "q", dt, (T, Hq, 128))
+    _ck(dev, K_pool, "K_pool", dt, pool)
+    _ck(dev, V_pool, "V_pool", dt, pool)
+    _ck(dev, page_table, "page_table", torch.int32, (B, max_pages))
+    _ck(dev, cu_q, "cu_q", torch.int32, (B + 1,))
+    _ck(dev, n_tokens_b, "n_tokens_b", torch.int32, (B,))
+    _ck(dev, out, "out", dt, (T, Hq, 128))
     if lse is not None:
-        _need(lse, "lse", torch.float32, shape=(T, Hq))
-    sc = _score(softcap, window, slopes, prefix_len, q_first, B, T, Hq)
-    _here(q, K_pool, V_pool, page_table, cu_q, n_tokens_b, out, lse, slopes, prefix_len, q_first, ws, status)
+        _ck(dev, lse, "lse", torch.float32, (T, Hq))
+    score = _score(dev, softcap, window, slopes, prefix_len, q_first, B, T, Hq)
+    ws_ptr, ws_bytes, status_ptr = _ck_ws(dev, ws, status)
     _ok(lib().hkv_prefill_attend_paged(
-        B, T, Hq, Hkv, _dtype_code(q), _ptr(q), _row_stride(q), _ptr(K_pool), _ptr(V_pool), _ptr(page_table),
-        page_table.shape[1], num_pages, page_size, _ptr(cu_q), _ptr(n_tokens_b), max_q, n_tokens_max,
-        1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+        B, T, Hq, Hkv, code, q.data_ptr(), q_stride, K_pool.data_ptr(), V_pool.data_ptr(), page_table.data_ptr(), max_pages,
+        num_pages, page_size, cu_q.data_ptr(), n_tokens_b.data_ptr(), max_q, n_tokens_max,
+        _SCALE if scale is None else scale, score, out.data_ptr(), _at(lse), ws_ptr, ws_bytes, status_ptr,
+        _raw_stream(stream, dev)))
 
 
 def hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, dtype: int) -> int:
@@ -845,9 +890,9 @@ def hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, dtype: int) -> i
 
 
 def shared_workspace(B, Hq, Hkv, n_prefix, n_own_max, dtype=torch.bfloat16, device=None) -> Optional[torch.Tensor]:
-    """A zero-filled workspace for hkv_shared_attend_paged, or None when this shape needs none."""
+    """The workspace of hkv_shared_attend_paged, or None when this shape needs none."""
     code = _dtype_code(torch.empty(0, dtype=dtype))
-    return _zeroed(hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, code), device)
+    return _scratch(hkv_shared_workspace_bytes(B, Hq, Hkv, n_prefix, n_own_max, code), device)
 
 
 def hkv_shared_attend_paged(q, K_pool, V_pool, prefix_table, n_prefix: int, page_table, n_own_b, n_own_max: int, out,
@@ -857,26 +902,29 @@ def hkv_shared_attend_paged(q, K_pool, V_pool, prefix_table, n_prefix: int, page
     q [B, Hq, 128] (rows may be strided); K_pool, V_pool [num_pages, Hkv, page_size, 128]; prefix_table [pages],
     page_table [B, max_pages] and n_own_b [B] int32 (each sequence's own tokens, its query the last of them);
     out [B, Hq, 128] in q's dtype; lse [B, Hq] fp32."""
-    B, Hq, d = q.shape
+    B, Hq, _ = q.shape
     num_pages, Hkv, page_size, _ = K_pool.shape
-    _need(q, "q", (torch.bfloat16, torch.float32), contiguous=False)
-    _need_rows(q, "q", q.dtype, (B, Hq, 128))
-    _need(K_pool, "K_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
-    _need(V_pool, "V_pool", q.dtype, shape=(num_pages, Hkv, page_size, 128))
-    _need(prefix_table, "prefix_table", torch.int32)
-    _need(page_table, "page_table", torch.int32)
+    dt, code = q.dtype, _row_dtype(q, "q")
     if prefix_table.dim() != 1:
         raise ValueError("prefix_table must be [prefix_pages]")
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B, max_pages]")
-    _need(n_own_b, "n_own_b", torch.int32, shape=(B,))
-    _need(out, "out", q.dtype, shape=(B, Hq, 128))
+    max_pages, prefix_pages = page_table.shape[1], prefix_table.shape[0]
+    dev = torch.cuda.current_device()
+    pool = (num_pages, Hkv, page_size, 128)
+    q_stride = _ck_rows(dev, q, "q", dt, (B, Hq, 128))
+    _ck(dev, K_pool, "K_pool", dt, pool)
+    _ck(dev, V_pool, "V_pool", dt, pool)
+    _ck(dev, prefix_table, "prefix_table", torch.int32, (prefix_pages,))
+    _ck(dev, page_table, "page_table", torch.int32, (B, max_pages))
+    _ck(dev, n_own_b, "n_own_b", torch.int32, (B,))
+    _ck(dev, out, "out", dt, (B, Hq, 128))
     if lse is not None:
-        _need(lse, "lse", torch.float32, shape=(B, Hq))
-    sc = _score(softcap, 0, slopes, None, None, B, B, Hq)
-    _here(q, K_pool, V_pool, prefix_table, page_table, n_own_b, out, lse, slopes, ws, status)
+        _ck(dev, lse, "lse", torch.float32, (B, Hq))
+    score = _score(dev, softcap, 0, slopes, None, None, B, B, Hq)
+    ws_ptr, ws_bytes, status_ptr = _ck_ws(dev, ws, status)
     _ok(lib().hkv_shared_attend_paged(
-        B, Hq, Hkv, _dtype_code(q), _ptr(q), _row_stride(q), _ptr(K_pool), _ptr(V_pool), _ptr(prefix_table),
-        prefix_table.shape[0], n_prefix, _ptr(page_table), page_table.shape[1], num_pages, page_size, _ptr(n_own_b),
-        n_own_max, 1.0 / math.sqrt(d) if scale is None else scale, ctypes.byref(sc), _ptr(out), _ptr(lse), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+        B, Hq, Hkv, code, q.data_ptr(), q_stride, K_pool.data_ptr(), V_pool.data_ptr(), prefix_table.data_ptr(), prefix_pages,
+        n_prefix, page_table.data_ptr(), max_pages, num_pages, page_size, n_own_b.data_ptr(), n_own_max,
+        _SCALE if scale is None else scale, score, out.data_ptr(), _at(lse), ws_ptr, ws_bytes, status_ptr,
+        _raw_stream(stream, dev)))

@@ -395,6 +395,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   const int first = lo < hi ? lo / kTile : 0, last = lo < hi ? (hi + kTile - 1) / kTile : 0;
   const int per = (last - first + t.splits - 1) / t.splits;
   const int t0 = first + split * per, t1 = min(last, t0 + per);
+  if (warp == 8 && lane < 8 && t0 + lane < t1)  // the page ids of the first tiles, while the barriers are set up
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(table + (uint32_t)(t0 + lane) * kTile / (uint32_t)a.pm.page_size));
   // the tiles that a slot works on
   auto run_of = [&](int s) -> Run {
     if (!both) return Run{t0 + s, t1, 2};
@@ -760,23 +762,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const int64_t out_row = (partial ? (t.part0 + split) * a.T * a.Hq : 0) + my_out;
       if (live && partial) a.part_ml[out_row] = make_float2(m, none ? 0.f : l);
       if (live && !partial && a.lse) a.lse[out_row] = none ? -INFINITY : (m + log2f(l)) * pa::kLn2;
-      // Rows leave through shared memory (the queries' place: this slot's MMAs
-      // are through with them), so that a row is written as whole lines: 256
-      // bytes of 32 rows at a time, 16-byte pieces swizzled by the row.
-      unsigned char* mine = smem + Layout::kQ + slot * kBuf + (warp & 3) * 8192;
-      unsigned char* dst = partial ? reinterpret_cast<unsigned char*>(a.part_o) : static_cast<unsigned char*>(a.out);
-      const int row_bytes = partial ? 512 : 256;
-      auto leave = [&](int at) {
-        __syncwarp();
-#pragma unroll 2
-        for (int x = lane >> 4; x < 32; x += 2) {
-          const int c = lane & 15;
-          const int64_t to = __shfl_sync(0xffffffffu, out_row, x);
-          const uint4 v = *reinterpret_cast<const uint4*>(mine + x * 256 + ((c ^ (x & 15)) << 4));
-          if (row - lane + x < nrows) *reinterpret_cast<uint4*>(dst + to * row_bytes + at + c * 16) = v;
-        }
-        __syncwarp();
-      };
       // one weight for the row's values: the sum, and in the other slot's favour
       const float w0 = none ? 0.f : scale0 * inv, w1 = none ? 0.f : scale1 * inv;
 #pragma unroll 1
@@ -790,19 +775,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         if (w1 > 0.f)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = fmaf(other[(32 * k + i) * kTile + row], w1, x[i]);
-        auto put = [&](int c, uint4 v) { *reinterpret_cast<uint4*>(mine + lane * 256 + ((c ^ (lane & 15)) << 4)) = v; };
-        if (partial) {
+        // a thread writes its own row, 64 or 128 bytes a step: whole lines by
+        // way of shared memory took as long
+        if (live && partial) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + out_row * kHeadDim + 32 * k);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            put((k & 1) * 8 + i, make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
-                                            __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3])));
-        } else {
+          for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + out_row * kHeadDim + 32 * k);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            put(4 * k + i, make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                      pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7])));
+            dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
         }
-        if (partial ? (k & 1) : k == 3) leave(partial ? (k >> 1) * 256 : 0);
       }
     }
   }

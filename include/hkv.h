@@ -548,11 +548,11 @@ typedef struct {
  *            them is cut to them and reported as HKV_ERR_DEVICE_RANGE
  *   score    nullable: plain causal attention
  *   out      [T, Hq, 128] in dtype;  lse nullable [T, Hq] fp32
- *   ws       hkv_prefill_workspace_bytes bytes, zeroed once before its first
- *            use (hkv_workspace_reset) and returned to that state by every
- *            call; the rules of hkv_workspace_bytes on sharing and other
- *            shapes hold.  A page id outside the pool is reported as
- * HKV_ERR_DEVICE_RANGE and its tokens are not attended. */
+ *   ws       hkv_prefill_workspace_bytes bytes (may be 0), 256-byte aligned; no
+ *            zero fill, and nothing in it outlives the call.  Calls that
+ *            share one must not overlap on the GPU
+ * A page id outside the pool is reported as HKV_ERR_DEVICE_RANGE and its
+ * tokens are not attended. */
 int hkv_prefill_attend_paged(int B, int64_t T, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride,
                              const void* K_pool, const void* V_pool, const int32_t* page_table, int64_t max_pages,
                              int64_t num_pages, int page_size, const int32_t* cu_q, const int32_t* n_tokens_b,
@@ -576,7 +576,7 @@ size_t hkv_prefill_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int dtype,
  *             and reported as HKV_ERR_DEVICE_RANGE
  *   score     nullable; softcap and slopes only (HKV_ERR_UNSUPPORTED otherwise)
  *   out       [B, Hq, 128] in dtype;  lse nullable [B, Hq] fp32
- *   ws        hkv_shared_workspace_bytes bytes, zeroed once, as above */
+ *   ws        hkv_shared_workspace_bytes bytes, as above */
 int hkv_shared_attend_paged(int B, int Hq, int Hkv, int dtype, const void* q, int64_t q_stride, const void* K_pool,
                             const void* V_pool, const int32_t* prefix_table, int64_t prefix_pages, int64_t n_prefix,
                             const int32_t* page_table, int64_t max_pages, int64_t num_pages, int page_size,
