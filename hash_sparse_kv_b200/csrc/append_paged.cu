@@ -32,6 +32,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRowLanes = 8;                     // lanes of one row
 constexpr int kKeyPitch = kHeadDim + 8;          // shared key rows: 272 bytes, conflict-free for ldmatrix
 constexpr int kMaxKeys = 64;                     // keys of a step in shared memory, unless one token has more
+// The projection's fragments leave room for two blocks per SM, with rows
+// further ahead; the others hide the memory's latency better with more warps.
+constexpr int blocks_per_sm(int hash) { return hash == 2 ? 3 : 4; }
 enum { kHashNone = 0, kHashSign = 1, kHashLsh = 2, kHashStage = 3 };
 
 struct AppendArgs {
@@ -57,51 +60,142 @@ template <typename T>
 struct Raw {
   uint4 v[sizeof(T) / 2];
 };
+// Eight values as four pairs: one instruction works on two.
 struct Chunk {
-  float x[8];
+  uint64_t x[4];
 };
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
 template <typename T>
 __device__ __forceinline__ Raw<T> load_raw(const T* p) {
   Raw<T> r;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
   return r;
 }
-__device__ __forceinline__ Chunk widen(const Raw<__nv_bfloat16>& r) {
-  Chunk c;
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+// Pair k is elements (2 k, 2 k + 1); with kZip, chunk `u` gets the even elements
+// of both chunks and `w` the odd ones, so that a pair of neighbours is one
+// element of each.
+template <bool kZip>
+__device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& a, const Raw<__nv_bfloat16>& b, Chunk& u, Chunk& w) {
+  const uint32_t p[8] = {a.v[0].x, a.v[0].y, a.v[0].z, a.v[0].w, b.v[0].x, b.v[0].y, b.v[0].z, b.v[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c.x[2 * i] = __uint_as_float(w[i] << 16);
-    c.x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (kZip) {
+      u.x[k] = pair(p[2 * k] << 16, p[2 * k + 1] << 16);
+      w.x[k] = pair(p[2 * k] & 0xffff0000u, p[2 * k + 1] & 0xffff0000u);
+    } else {
+      u.x[k] = pair(p[k] << 16, p[k] & 0xffff0000u);
+      w.x[k] = pair(p[4 + k] << 16, p[4 + k] & 0xffff0000u);
+    }
   }
-  return c;
 }
-__device__ __forceinline__ Chunk widen(const Raw<float>& r) {
-  return Chunk{{__uint_as_float(r.v[0].x), __uint_as_float(r.v[0].y), __uint_as_float(r.v[0].z), __uint_as_float(r.v[0].w),
-                __uint_as_float(r.v[1].x), __uint_as_float(r.v[1].y), __uint_as_float(r.v[1].z), __uint_as_float(r.v[1].w)}};
-}
-__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const Chunk& c) {
-  uint32_t w[4];
+template <bool kZip>
+__device__ __forceinline__ void widen(const Raw<float>& a, const Raw<float>& b, Chunk& u, Chunk& w) {
+  const uint4 q[4] = {a.v[0], a.v[1], b.v[0], b.v[1]};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(c.x[2 * i], c.x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (kZip) {
+      u.x[k] = pair(q[k].x, q[k].z), w.x[k] = pair(q[k].y, q[k].w);
+      u.x[2 + k] = pair(q[2 + k].x, q[2 + k].z), w.x[2 + k] = pair(q[2 + k].y, q[2 + k].w);
+    } else {
+      u.x[2 * k] = pair(q[k].x, q[k].y), u.x[2 * k + 1] = pair(q[k].z, q[k].w);
+      w.x[2 * k] = pair(q[2 + k].x, q[2 + k].y), w.x[2 * k + 1] = pair(q[2 + k].z, q[2 + k].w);
+    }
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store_chunk(float* p, const Chunk& c) {
-  *reinterpret_cast<float4*>(p) = make_float4(c.x[0], c.x[1], c.x[2], c.x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(c.x[4], c.x[5], c.x[6], c.x[7]);
+// Back to memory order, rounded to the type.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
-// the value that the cache holds for x
-__device__ __forceinline__ float stored(float x, const __nv_bfloat16*) { return __bfloat162float(__float2bfloat16_rn(x)); }
-__device__ __forceinline__ float stored(float x, const float*) { return x; }
+template <bool kZip>
+__device__ __forceinline__ void narrow(const Chunk& u, const Chunk& w, Raw<__nv_bfloat16>& a, Raw<__nv_bfloat16>& b) {
+  uint32_t p[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = unpair(u.x[k]), y = unpair(w.x[k]);
+    if constexpr (kZip)
+      p[2 * k] = bf16_pair(x.x, y.x), p[2 * k + 1] = bf16_pair(x.y, y.y);
+    else
+      p[k] = bf16_pair(x.x, x.y), p[4 + k] = bf16_pair(y.x, y.y);
+  }
+  a.v[0] = make_uint4(p[0], p[1], p[2], p[3]), b.v[0] = make_uint4(p[4], p[5], p[6], p[7]);
+}
+template <bool kZip>
+__device__ __forceinline__ void narrow(const Chunk& u, const Chunk& w, Raw<float>& a, Raw<float>& b) {
+  float p[16];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = unpair(u.x[k]), y = unpair(w.x[k]);
+    if constexpr (kZip)
+      p[4 * k] = x.x, p[4 * k + 1] = y.x, p[4 * k + 2] = x.y, p[4 * k + 3] = y.y;
+    else
+      p[2 * k] = x.x, p[2 * k + 1] = x.y, p[8 + 2 * k] = y.x, p[8 + 2 * k + 1] = y.y;
+  }
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  a.v[0] = q[0], a.v[1] = q[1], b.v[0] = q[2], b.v[1] = q[3];
+}
+template <typename T>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+}
+// element k of a stored chunk
+__device__ __forceinline__ float element(const Raw<__nv_bfloat16>& r, int k) {
+  const uint32_t p[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+  return __uint_as_float(k & 1 ? p[k / 2] & 0xffff0000u : p[k / 2] << 16);
+}
+__device__ __forceinline__ float element(const Raw<float>& r, int k) {
+  const uint32_t p[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+  return __uint_as_float(p[k]);
+}
 
-__device__ __forceinline__ void turn(float& lo, float& hi, float2 cs) {
-  const float a = __fsub_rn(__fmul_rn(lo, cs.x), __fmul_rn(hi, cs.y));
-  hi = __fadd_rn(__fmul_rn(hi, cs.x), __fmul_rn(lo, cs.y));
-  lo = a;
+// Products and sums rounded one by one, two at a time.
+__device__ __forceinline__ void turn(uint64_t& lo, uint64_t& hi, uint64_t c, uint64_t s) {
+  uint64_t a, b, d, e;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a) : "l"(lo), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(b) : "l"(hi), "l"(s));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(hi), "l"(c));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(e) : "l"(lo), "l"(s));
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(lo) : "l"(a), "l"(b));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(hi) : "l"(d), "l"(e));
+}
+
+// Sine and cosine in fp64 of any angle below 2^31 turns: the nearest multiple n
+// of pi / 2 is taken off in two fused steps (the second constant is what the
+// first one lacks), and the Taylor series on [-pi / 4, pi / 4] up to r^13 and
+// r^14 are off by less than 2^-45, far below the fp32 results' own rounding.
+__device__ __forceinline__ float2 cos_sin(double angle) {
+  const double n = rint(angle * 0.63661977236758134);
+  double r = fma(-n, 1.5707963267948966, angle);
+  r = fma(-n, 6.123233995736766e-17, r);
+  const double z = r * r;
+  double s = fma(z, 1.0 / 6227020800.0, -1.0 / 39916800.0);
+  s = fma(z, s, 1.0 / 362880.0);
+  s = fma(z, s, -1.0 / 5040.0);
+  s = fma(z, s, 1.0 / 120.0);
+  s = fma(z, s, -1.0 / 6.0);
+  s = fma(r * z, s, r);
+  double c = fma(z, -1.0 / 87178291200.0, 1.0 / 479001600.0);
+  c = fma(z, c, -1.0 / 3628800.0);
+  c = fma(z, c, 1.0 / 40320.0);
+  c = fma(z, c, -1.0 / 720.0);
+  c = fma(z, c, 1.0 / 24.0);
+  c = fma(z, c, -0.5);
+  c = fma(z, c, 1.0);
+  const float fs = (float)s, fc = (float)c;
+  const uint32_t q = (uint32_t)(int64_t)n & 3u;
+  const float x = q & 1u ? fs : fc, y = q & 1u ? fc : fs;
+  return make_float2(q == 1u || q == 2u ? -x : x, q & 2u ? -y : y);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const void* p) {
@@ -139,10 +233,10 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t) {
 // sum of bf16 squares is off by less than 8e-6, which matters only next to a
 // rounding border; there, and for fp32 rows, the fp64 sum decides.
 template <typename T>
-__device__ __forceinline__ uint16_t row_norm(const Chunk& u, const Chunk& w) {
+__device__ __forceinline__ uint16_t row_norm(const Raw<T>& a, const Raw<T>& b) {
   float ss = 0.f;
 #pragma unroll
-  for (int z = 0; z < 8; ++z) ss = fmaf(u.x[z], u.x[z], fmaf(w.x[z], w.x[z], ss));
+  for (int z = 0; z < 8; ++z) ss = fmaf(element(a, z), element(a, z), fmaf(element(b, z), element(b, z), ss));
 #pragma unroll
   for (int o = 1; o < kRowLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const float n = sqrtf(ss);
@@ -150,8 +244,14 @@ __device__ __forceinline__ uint16_t row_norm(const Chunk& u, const Chunk& w) {
   uint16_t out = hi;
   if (__any_sync(0xffffffffu, sizeof(T) == 4 || lo != hi)) {
     double d = 0.0;
+#pragma unroll 1
+    for (int z = 0; z < 8; ++z) {
+      float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int z = 0; z < 8; ++z) d = fma((double)u.x[z], (double)u.x[z], fma((double)w.x[z], (double)w.x[z], d));
+      for (int k = 0; k < 8; ++k)
+        if (k == z) x = element(a, k), y = element(b, k);
+      d = fma((double)x, (double)x, fma((double)y, (double)y, d));
+    }
 #pragma unroll
     for (int o = 1; o < kRowLanes; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     out = __half_as_ushort(__double2half(sqrt(d)));
@@ -160,11 +260,11 @@ __device__ __forceinline__ uint16_t row_norm(const Chunk& u, const Chunk& w) {
 }
 
 template <typename T, int HASH>
-__global__ void __launch_bounds__(kThreads, HASH == kHashLsh ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(HASH))
 append_paged_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int D = kHeadDim;
+  constexpr int D = kHeadDim, kAhead = blocks_per_sm(HASH) == 2 ? 2 : 1;  // groups of four rows that a warp has on their way
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ __align__(16) float2 cs_s[kWarps][64];  // (cos, sin) of a warp's token
+  __shared__ __align__(16) float cos_s[kWarps][64], sin_s[kWarps][64];  // of a warp's token
   __shared__ int64_t row_s[2][kWarps];               // kHashLsh: pool rows of a step's tokens
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = lane % kRowLanes, sub = lane / kRowLanes;
@@ -180,18 +280,10 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
   const int key_rows = (tokens * a.Hkv + 15) / 16 * 16;
   __nv_bfloat16* keys = reinterpret_cast<__nv_bfloat16*>(smem);  // kHashLsh: [2][key_rows][kKeyPitch]
   const int ntile = HASH == kHashLsh ? a.words / 2 : 0;          // n8 tiles per warp: 2 or 1
-  uint32_t rb[2][8][2];
+  __nv_bfloat16* R_s = keys + 2 * key_rows * kKeyPitch;           // kHashLsh: [bits][kKeyPitch]
   if constexpr (HASH == kHashLsh) {
-    const __nv_bfloat16* R = static_cast<const __nv_bfloat16*>(a.R);
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const int bit = (warp * ntile + n) * 8 + lane / 4;
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(R + (int64_t)bit * D + kk * 16) + lane % 4;
-        rb[n][kk][0] = n < ntile ? __ldg(p) : 0u;
-        rb[n][kk][1] = n < ntile ? __ldg(p + 4) : 0u;
-      }
+    for (int i = tid; i < a.words * 32 * (D / 8); i += kThreads)
+      *reinterpret_cast<uint4*>(R_s + i / (D / 8) * kKeyPitch + i % (D / 8) * 8) = __ldg(static_cast<const uint4*>(a.R) + i);
     // rows behind a step's last key are multiplied too: give them a value
     for (int i = tid; i < 2 * key_rows * kKeyPitch; i += kThreads) keys[i] = __nv_bfloat16(0.f);
     __syncthreads();
@@ -211,11 +303,12 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
         heads = is_q ? a.Hq : a.Hkv;
         return (is_q ? xq : is_k ? xk : xv) + head * D;
       };
-      int head, heads;
-      Raw<T> ra{}, rw{};
-      {
-        const T* src = row_of(part, head, heads);
-        if (part < all4 && head < heads) ra = load_raw(src + c0), rw = load_raw(src + c1);
+      Raw<T> ra[kAhead], rw[kAhead];  // the next groups, on their way
+      int head[kAhead], heads[kAhead];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) {
+        const T* src = row_of(part + e * a.parts, head[e], heads[e]);
+        if (part + e * a.parts < all4 && head[e] < heads[e]) ra[e] = load_raw(src + c0), rw[e] = load_raw(src + c1);
       }
       const Place at = place_of(a, t);
       if (lane == 0 && part == 0) {
@@ -225,64 +318,60 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
       if (at.row != -1) {
         for (int p = lane; p < a.pairs; p += 32) {
           const int pos = a.positions ? __ldg(a.positions + (int64_t)a.axis[p] * a.T + t) : at.pos;
-          const double ang = (double)pos * (double)__ldg(a.inv_freq + p);
-          const double n = rint(ang * 0.15915494309189535);
-          double r = fma(-n, 6.283185307179586, ang);
-          r = fma(-n, 2.4492935982947064e-16, r);
-          double s, co;
-          sincos(r, &s, &co);
-          cs_s[warp][p] = make_float2((float)co, (float)s);
+          const float2 cs = cos_sin((double)pos * (double)__ldg(a.inv_freq + p));
+          cos_s[warp][p] = cs.x, sin_s[warp][p] = cs.y;
         }
         __syncwarp();
-        float2 cs[8];
+        uint64_t cs[4], sn[4];
         if (turned) {
+          // pairs 8 c .. 8 c + 7 (neighbours: those of both chunks in order)
 #pragma unroll
-          for (int z = 0; z < 8; z += 2) {
-            const float4 x = *reinterpret_cast<const float4*>(&cs_s[warp][c * 8 + z]);
-            cs[z] = make_float2(x.x, x.y), cs[z + 1] = make_float2(x.z, x.w);
+          for (int z = 0; z < 4; ++z) {
+            cs[z] = *reinterpret_cast<const uint64_t*>(&cos_s[warp][c * 8 + 2 * z]);
+            sn[z] = *reinterpret_cast<const uint64_t*>(&sin_s[warp][c * 8 + 2 * z]);
           }
         }
         __syncwarp();
         T* const oq = static_cast<T*>(a.q_out) + t * a.qo_stride;
-#pragma unroll 1
-        for (int i = part; i < all4; i += a.parts) {
-          const Raw<T> xa = ra, xw = rw;
-          const int h = head;
-          const bool is_q = i < q4, is_k = !is_q && i < q4 + k4, in = h < heads && (is_q || at.row >= 0);
-          if (i + a.parts < all4) {
-            const T* src = row_of(i + a.parts, head, heads);
-            if (head < heads) ra = load_raw(src + c0), rw = load_raw(src + c1);
+        for (int i0 = part; i0 < all4; i0 += kAhead * a.parts) {
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+          const int i = i0 + e * a.parts;
+          if (i >= all4) break;
+          Raw<T> xa = ra[e], xw = rw[e];
+          const int h = head[e];
+          const bool is_q = i < q4, is_k = !is_q && i < q4 + k4, in = h < heads[e] && (is_q || at.row >= 0);
+          {
+            const int next = i + kAhead * a.parts;
+            const T* src = row_of(next, head[e], heads[e]);
+            if (next < all4 && head[e] < heads[e]) ra[e] = load_raw(src + c0), rw[e] = load_raw(src + c1);
           }
           T* dst = is_q ? oq + h * D : static_cast<T*>(is_k ? a.K : a.V) + (at.row + (int64_t)h * a.pm.page_size) * D;
-          Chunk u = widen(xa), w = widen(xw);
           if (turned && (is_q || is_k)) {
+            Chunk u, w;
             if (split) {
+              widen<false>(xa, xw, u, w);
 #pragma unroll
-              for (int z = 0; z < 8; ++z) turn(u.x[z], w.x[z], cs[z]);
+              for (int z = 0; z < 4; ++z) turn(u.x[z], w.x[z], cs[z], sn[z]);
+              narrow<false>(u, w, xa, xw);
             } else {
+              widen<true>(xa, xw, u, w);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                turn(u.x[2 * z], u.x[2 * z + 1], cs[z]);
-                turn(w.x[2 * z], w.x[2 * z + 1], cs[4 + z]);
-              }
+              for (int z = 0; z < 4; ++z) turn(u.x[z], w.x[z], cs[z], sn[z]);
+              narrow<true>(u, w, xa, xw);
             }
           }
-          if (in) {
-            store_chunk(dst + c0, u);
-            store_chunk(dst + c1, w);
-          }
+          if (in) store_raw(dst + c0, xa), store_raw(dst + c1, xw);
           if constexpr (HASH == kHashLsh) {
             if (is_k && in) {
               T* kd = reinterpret_cast<T*>(keys + (buf * key_rows + warp / a.parts * a.Hkv + h) * kKeyPitch);
-              store_chunk(kd + c0, u);
-              store_chunk(kd + c1, w);
+              store_raw(kd + c0, xa), store_raw(kd + c1, xw);
             }
           }
           if constexpr (HASH == kHashStage) {
             if (is_k && in) {
               T* kd = static_cast<T*>(a.staged) + (t * a.Hkv + h) * D;
-              store_chunk(kd + c0, u);
-              store_chunk(kd + c1, w);
+              store_raw(kd + c0, xa), store_raw(kd + c1, xw);
             }
           }
           if constexpr (HASH == kHashSign) {
@@ -290,14 +379,10 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
               uint32_t word[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                Chunk& x = half ? w : u;
                 const int ch = (half ? c1 : c0) / 8;
                 uint32_t byte = 0;
 #pragma unroll
-                for (int z = 0; z < 8; ++z) {
-                  x.x[z] = stored(x.x[z], static_cast<const T*>(nullptr));
-                  byte |= (uint32_t)(x.x[z] > 0.f) << z;
-                }
+                for (int z = 0; z < 8; ++z) byte |= (uint32_t)(element(half ? xw : xa, z) > 0.f) << z;
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
                   if (ch / 4 == z) word[z] |= byte << (8 * (ch % 4));
@@ -309,11 +394,12 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
               const int64_t row = at.row + (int64_t)h * a.pm.page_size;
               if (in && c == 0) *reinterpret_cast<uint4*>(a.codes + row * 4) = make_uint4(word[0], word[1], word[2], word[3]);
               if (a.norms) {
-                const uint16_t norm = row_norm<T>(u, w);
+                const uint16_t norm = row_norm<T>(xa, xw);
                 if (in && c == 0) a.norms[row] = norm;
               }
             }
           }
+        }
         }
       }
     }
@@ -326,8 +412,11 @@ append_paged_kernel(const __grid_constant__ AppendArgs a) {
         for (int kk = 0; kk < 8; ++kk) {
           uint32_t af[4];
           ldsm4(af, keys + (buf * key_rows + m0 + lane % 16) * kKeyPitch + kk * 16 + (lane / 16) * 8);
-          mma16816(y[0], af, rb[0][kk][0], rb[0][kk][1]);
-          if (ntile == 2) mma16816(y[1], af, rb[1][kk][0], rb[1][kk][1]);
+          uint32_t bf[4];  // both tiles of 8 bits, k halves next to each other
+          const int bit = (warp * ntile + (ntile == 2 ? lane >> 4 : 0)) * 8 + (lane & 7);
+          ldsm4(bf, R_s + bit * kKeyPitch + kk * 16 + ((lane >> 3) & 1) * 8);
+          mma16816(y[0], af, bf[0], bf[1]);
+          if (ntile == 2) mma16816(y[1], af, bf[2], bf[3]);
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // rows lane / 4 and lane / 4 + 8
@@ -385,13 +474,13 @@ int run_append(const AppendArgs& a, int hash, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     if (hash == kHashLsh) {
       kernel = append_paged_kernel<T, kHashLsh>;
-      smem = 2 * align_up((size_t)(kWarps / a.parts) * a.Hkv, 16) * kKeyPitch * sizeof(T);
+      smem = (2 * align_up((size_t)(kWarps / a.parts) * a.Hkv, 16) + a.words * 32) * kKeyPitch * sizeof(T);
       if (smem + 8192 > (size_t)max_smem_optin()) return fail(HKV_ERR_UNSUPPORTED, "Hkv %d too large", a.Hkv);
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return cuda_check(e, "append smem attribute");
     }
   }
-  const int64_t steps = ceil_div(a.T, kWarps / a.parts), most = (int64_t)sm_count() * (hash == kHashLsh ? 2 : 3);
+  const int64_t steps = ceil_div(a.T, kWarps / a.parts), most = (int64_t)sm_count() * blocks_per_sm(hash);
   kernel<<<(unsigned)(steps < most ? steps : most), kThreads, smem, st>>>(a);
   return cuda_check(cudaGetLastError(), "append launch");
 }
