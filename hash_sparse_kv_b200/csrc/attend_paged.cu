@@ -92,112 +92,175 @@ __device__ void finish(const Args& a, const Item& it, const float* o_s, const fl
   }
 }
 
-template <typename T, bool kPrefix>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+// fp32: eight warps, tiles of 32 tokens staged in shared memory (cp.async, two
+// tiles ahead, their places looked up one tile before that).  A warp has two rows to itself: lane u scores
+// them against token u, then holds four output columns of each, so that only
+// the staging makes warps wait for each other.  Bound by the shared memory
+// reads of the two products; two rows a warp and 16-byte reads keep them at
+// three for 16 multiply-adds, which go two to an instruction.
+constexpr int kSimtStages = 3, kSimtKPitch = kHeadDim + 4;
+struct SimtStage {
+  float k[kTile][kSimtKPitch];
+  float v[kTile][kHeadDim];
+  bool there[kTile];
+};
+
+template <bool kPrefix>
+__global__ void __launch_bounds__(kThreads, 2)
 rows_simt_kernel(const __grid_constant__ Args a) {
-  constexpr int D = kHeadDim, KP = D + 1;
+  constexpr int D = kHeadDim;
+  static_assert(kRows == 2 * (kThreads / 32) && kTile == 32, "two rows a warp, a token a lane");
   __shared__ __align__(16) float q_s[kRows][D];  // the block's result in the end
-  __shared__ __align__(16) float k_s[kTile][KP];
-  __shared__ __align__(16) float v_s[kTile][D];
-  __shared__ float p_s[kRows][kTile];
-  __shared__ float m_s[kRows], l_s[kRows], f_s[kRows];
-  __shared__ int64_t row_s[kTile];
-  const int tid = threadIdx.x;
+  __shared__ __align__(16) float p_s[kRows][kTile];
+  __shared__ float m_s[kRows], l_s[kRows];
+  extern __shared__ __align__(16) unsigned char simt_smem[];
+  SimtStage* const stages = reinterpret_cast<SimtStage*>(simt_smem);
+  __shared__ int lo_s, hi_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Item it;
   if (!item_of<kPrefix>(a, it)) return;
-  for (int i = tid; i < kRows * D; i += kThreads) {
-    const int r = i / D, d = i % D;
-    const T* q = static_cast<const T*>(a.q) + (it.row0 + r / a.g) * a.q_stride + (int64_t)(it.j * a.g + r % a.g) * D;
-    q_s[r][d] = r < it.nrows ? to_f32(q[d]) : 0.f;
-  }
-  // thread (r, u) scores row r against tokens u and u + 16 of a tile
-  const int r = tid / 16, u = tid % 16;
-  pa::Span sp{0, 0, 0};
-  if (r < it.nrows) sp = row_span<kPrefix>(a, it, r);
-  const float slope = a.slopes && r < it.nrows ? a.slopes[it.j * a.g + r % a.g] * pa::kLog2e : 0.f;
-  __shared__ int lo_s, hi_s;
   if (tid == 0) lo_s = INT32_MAX, hi_s = 0;
-  if (u == 0) m_s[r] = -INFINITY, l_s[r] = 0.f;
+  pa::Span sp[2];
+  float slope[2];
+  const int r0 = warp * 2;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + h;
+    const float* q = static_cast<const float*>(a.q) + (it.row0 + r / a.g) * a.q_stride + (int64_t)(it.j * a.g + r % a.g) * D;
+    *reinterpret_cast<float4*>(&q_s[r][lane * 4]) =
+        r < it.nrows ? __ldg(reinterpret_cast<const float4*>(q) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    sp[h] = r < it.nrows ? row_span<kPrefix>(a, it, r) : pa::Span{0, 0, 0};
+    slope[h] = a.slopes && r < it.nrows ? a.slopes[it.j * a.g + r % a.g] * pa::kLog2e : 0.f;
+  }
   __syncthreads();
-  if (u == 0 && sp.lo < sp.hi) {
-    atomicMin(&lo_s, sp.lo);
-    atomicMax(&hi_s, sp.hi);
+  if (lane < 2) {
+    const pa::Span x = lane ? sp[1] : sp[0];
+    if (x.lo < x.hi) {
+      atomicMin(&lo_s, x.lo);
+      atomicMax(&hi_s, x.hi);
+    }
   }
   __syncthreads();
   const int lo = min(lo_s, hi_s), hi = hi_s;
   const int tiles = (hi - lo + kTile - 1) / kTile, per = (tiles + gridDim.z - 1) / gridDim.z;
-  const int t_end = min(tiles, ((int)blockIdx.z + 1) * per);
+  const int t0 = blockIdx.z * per, t1 = min(tiles, t0 + per);
   const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)it.b * a.pm.max_pages;
-  float acc[8] = {};
-  const int col = tid % D, ar0 = tid / D * 8;
-  for (int t = blockIdx.z * per; t < t_end; ++t) {
-    const int u0 = lo + t * kTile;
-    __syncthreads();
-    if (tid < kTile) {
-      row_s[tid] = u0 + tid < hi ? pa::pool_row(a, table, u0 + tid, it.j) : -1;
-      if (u0 + tid < hi && row_s[tid] < 0) report(a.status, HKV_ERR_DEVICE_RANGE);
-    }
-    __syncthreads();
-    for (int i = tid; i < kTile * (D / 4); i += kThreads) {
-      const int x = i / (D / 4), d = i % (D / 4) * 4;
-      float4 k4 = make_float4(0.f, 0.f, 0.f, 0.f), v4 = k4;
-      if (row_s[x] >= 0) {
-        k4 = load4_f32(static_cast<const T*>(a.K) + row_s[x] * D + d);
-        v4 = load4_f32(static_cast<const T*>(a.V) + row_s[x] * D + d);
+  // this thread moves piece tid % 32 of tokens tid / 32 + 8 k
+  const int x0 = tid / 32, piece = tid % 32 * 4;
+  // lane u looks up token u of a tile
+  auto row_at = [&](int t) -> int64_t {
+    const int at = lo + t * kTile + lane;
+    if (t >= t1 || at >= hi) return -1;
+    const int64_t row = pa::pool_row(a, table, at, it.j);
+    if (row < 0) report(a.status, HKV_ERR_DEVICE_RANGE);
+    return row;
+  };
+  int64_t row = row_at(t0);
+  int ahead = t0, to = 0;
+  auto fetch_next = [&] {
+    if (ahead < t1) {
+      SimtStage& st = stages[to];
+      if (warp == 0) st.there[lane] = row >= 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t from = __shfl_sync(0xffffffffu, row, x0 + 8 * k);
+        const int64_t off = from >= 0 ? from * D + piece : 0;
+        cp16(sm32(&st.k[x0 + 8 * k][piece]), static_cast<const float*>(a.K) + off, from >= 0 ? 16 : 0);
+        cp16(sm32(&st.v[x0 + 8 * k][piece]), static_cast<const float*>(a.V) + off, from >= 0 ? 16 : 0);
       }
-      k_s[x][d] = k4.x, k_s[x][d + 1] = k4.y, k_s[x][d + 2] = k4.z, k_s[x][d + 3] = k4.w;
-      *reinterpret_cast<float4*>(&v_s[x][d]) = v4;
     }
-    __syncthreads();
-    float z[2] = {0.f, 0.f};
-#pragma unroll 8
-    for (int d = 0; d < D; ++d) {
-      const float q = q_s[r][d];
-      z[0] = fmaf(q, k_s[u][d], z[0]);
-      z[1] = fmaf(q, k_s[u + 16][d], z[1]);
-    }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int x = u + 16 * e, pos = u0 + x;
-      float s = z[e] * a.scale;
-      if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-      s = s * pa::kLog2e - slope * (float)abs(sp.pos - pos);
-      z[e] = pos >= sp.lo && pos < sp.hi && row_s[x] >= 0 ? s : -INFINITY;
-      mx = fmaxf(mx, z[e]);
-    }
-#pragma unroll
-    for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float m_old = m_s[r], m_new = fmaxf(m_old, mx), m_use = m_new == -INFINITY ? 0.f : m_new;
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float p = exp2f(z[e] - m_use);
-      p_s[r][u + 16 * e] = p;
-      sum += p;
-    }
-#pragma unroll
-    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
-    if (u == 0) {
-      const float f = exp2f(m_old - m_use);
-      f_s[r] = f, m_s[r] = m_new, l_s[r] = l_s[r] * f + sum;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) acc[k] *= f_s[ar0 + k];
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    row = row_at(++ahead);
+    if (++to == kSimtStages) to = 0;
+  };
+  uint64_t acc[2][2] = {};  // rows r0 and r0 + 1, columns 4 lane .. 4 lane + 3
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+  for (int k = 0; k < kSimtStages - 1; ++k) fetch_next();
+  int at = 0;
+  for (int t = t0; t < t1; ++t) {
+    const int pos = lo + t * kTile + lane;
+    const SimtStage& st = stages[at];
+    if (++at == kSimtStages) at = 0;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSimtStages - 2) : "memory");
+    __syncthreads();  // this tile is there; the one before it has been used
+    fetch_next();
+    uint64_t z2[2][2] = {};
 #pragma unroll 4
-    for (int x = 0; x < kTile; ++x) {
-      const float v = v_s[x][col];
+    for (int d = 0; d < D; d += 4) {
+      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&st.k[lane][d]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = fmaf(p_s[ar0 + k][x], v, acc[k]);
+      for (int h = 0; h < 2; ++h) {
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&q_s[r0 + h][d]);
+        z2[h][0] = fma2(q.x, k.x, z2[h][0]);
+        z2[h][1] = fma2(q.y, k.y, z2[h][1]);
+      }
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 x = unpair(z2[h][0]), y = unpair(z2[h][1]);
+      float s = ((x.x + x.y) + (y.x + y.y)) * a.scale;
+      if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
+      s = s * pa::kLog2e - slope[h] * (float)abs(sp[h].pos - pos);
+      if (pos < sp[h].lo || pos >= sp[h].hi || !st.there[lane]) s = -INFINITY;
+      float top = s;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = fmaxf(m[h], top), use = mn == -INFINITY ? 0.f : mn;
+      const float p = exp2f(s - use), f = exp2f(m[h] - use);
+      p_s[r0 + h][lane] = p;
+      l[h] = l[h] * f + p;  // this lane's tokens; the lanes' sums meet in the end
+      m[h] = mn;
+      const uint64_t f2 = pair(f, f);
+      acc[h][0] = fma2(acc[h][0], f2, 0), acc[h][1] = fma2(acc[h][1], f2, 0);
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int x = 0; x < kTile; x += 4) {
+      const float4 pa4 = *reinterpret_cast<const float4*>(&p_s[r0][x]), pb4 = *reinterpret_cast<const float4*>(&p_s[r0 + 1][x]);
+      const float pr[2][4] = {{pa4.x, pa4.y, pa4.z, pa4.w}, {pb4.x, pb4.y, pb4.z, pb4.w}};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&st.v[x + e][lane * 4]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint64_t p2 = pair(pr[h][e], pr[h][e]);
+          acc[h][0] = fma2(p2, v.x, acc[h][0]);
+          acc[h][1] = fma2(p2, v.y, acc[h][1]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+    *reinterpret_cast<ulonglong2*>(&q_s[r0 + h][lane * 4]) = make_ulonglong2(acc[h][0], acc[h][1]);  // this warp's own rows
+    if (lane == 0) m_s[r0 + h] = m[h], l_s[r0 + h] = l[h];
   }
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 8; ++k) q_s[ar0 + k][col] = acc[k];
-  __syncthreads();
-  finish<T, kPrefix>(a, it, q_s[0], m_s, l_s);
+  finish<float, kPrefix>(a, it, q_s[0], m_s, l_s);
 }
 
 // ---- bf16: the same on the tensor cores of one warp --------------------------
@@ -215,10 +278,6 @@ constexpr int kStepBytes = kStep * 256;      // of K, and again of V
 constexpr int kQPitch = kHeadDim + 8;
 constexpr size_t kMmaSmem = (size_t)kMmaWarps * kStages * 2 * kStepBytes;
 
-__device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(p) : "memory");
@@ -572,7 +631,11 @@ int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
   } else {
     if (pl.prefix_parts > 0) {
       if constexpr (sizeof(T) == 4) {
-        rows_simt_kernel<T, true><<<dim3((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts), kThreads, 0, st>>>(a);
+        rc = cuda_check(cudaFuncSetAttribute(rows_simt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(kSimtStages * sizeof(SimtStage))), "prefix attention smem attribute");
+        if (rc != HKV_OK) return rc;
+        rows_simt_kernel<true><<<dim3((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts), kThreads,
+                                 kSimtStages * sizeof(SimtStage), st>>>(a);
         rc = cuda_check(cudaGetLastError(), "prefix attention launch");
       } else {
         rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
@@ -591,7 +654,10 @@ int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
       }
       rc = cuda_check(e, "paged attention launch");
     } else {
-      rows_simt_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
+      rc = cuda_check(cudaFuncSetAttribute(rows_simt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)(kSimtStages * sizeof(SimtStage))), "paged attention smem attribute");
+      if (rc != HKV_OK) return rc;
+      rows_simt_kernel<false><<<grid, kThreads, kSimtStages * sizeof(SimtStage), st>>>(a);
       rc = cuda_check(cudaGetLastError(), "paged attention launch");
     }
   }
