@@ -160,17 +160,25 @@ __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
   return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(n.x) << 23)),
                      __int_as_float(__float_as_int(v.y) + (__float_as_int(n.y) << 23)));
 }
-// tanh on [-1, 1] for two values: odd minimax polynomial of degree 13,
-// absolute error 1e-7.
-__device__ __forceinline__ uint64_t tanh_poly(uint64_t x) {
-  const float c[7] = {9.999997020e-01f, -3.333213031e-01f, 1.331958324e-01f, -5.326583236e-02f,
-                      1.997327618e-02f, -5.951274652e-03f, 9.637702024e-04f};
-  const uint64_t u = mul2(x, x);
-  uint64_t p = pair(c[6], c[6]);
+// cap * tanh(f v) for |f v| <= 1/2, as v * (c0 + c1 v^2 + c2 v^4 + c3 v^6): the odd
+// minimax polynomial of degree 7 (absolute error of the tanh 1.6e-7), with f
+// and cap multiplied into its coefficients once.
+struct CapPoly {
+  float c[4];
+  __device__ __forceinline__ CapPoly(float f, float cap) {
+    const float t[4] = {9.999976754e-01f, -3.332065642e-01f, 1.314514428e-01f, -4.337245598e-02f};
+    float power = f * cap;
 #pragma unroll
-  for (int i = 5; i >= 0; --i) p = fma2(p, u, pair(c[i], c[i]));
-  return mul2(p, x);
-}
+    for (int i = 0; i < 4; ++i) c[i] = t[i] * power, power *= f * f;
+  }
+  __device__ __forceinline__ uint64_t factor(uint64_t v) const {
+    const uint64_t u = mul2(v, v);
+    uint64_t p = pair(c[3], c[3]);
+#pragma unroll
+    for (int i = 2; i >= 0; --i) p = fma2(p, u, pair(c[i], c[i]));
+    return p;
+  }
+};
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -564,6 +572,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // (biased) the score itself
     const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f, cap = a.softcap * pa::kLog2e;
     const float c = kMode == kPlain ? a.scale * pa::kLog2e : kMode == kCapped ? cap : 1.f;
+    const CapPoly poly(to_cap, cap);
     const float slope = kMode == kBiased && a.slopes && live ? a.slopes[j * a.g + head] * pa::kLog2e : 0.f;
     for (int n = run.first; active && n < run.last; n += run.step) {
       const bool ok = wait(&s_full[slot], done & 1, abort, a.wait_ns);
@@ -630,14 +639,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       };
       extremes();
       if constexpr (kMode == kCapped) {
-        // the polynomial serves while no score of the warp is past the cap
-        if (!formed && !all(fmaxf(top, -low) * fabsf(to_cap) <= 1.f)) {
+        // the polynomial serves while the warp's scores are below half the cap
+        if (!formed && !all(fmaxf(top, -low) * fabsf(to_cap) <= 0.5f)) {
           form(), formed = true;
           extremes();
         }
         if (!formed) {
-          const float t = to_cap > 0.f ? top : low;
-          top = unpair(tanh_poly(pair(t * to_cap, 0.f))).x;
+          const float x = to_cap > 0.f ? top : low;
+          top = x * unpair(poly.factor(pair(x, x))).x / c;
         }
       }
       top *= c;  // c is positive: the largest value is the largest score
@@ -669,15 +678,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const float off = m == -INFINITY ? 0.f : m;
       uint64_t sum[2] = {0, 0};
       const uint64_t c2 = pair(c, c), off2 = pair(-off, -off);
-      const uint64_t cap2 = pair(to_cap, to_cap);
       // 32 scores to weights
       auto weigh = [&](const uint32_t(&v)[32], int k, auto raw) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           uint64_t z = pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-          if constexpr (decltype(raw)::value) z = tanh_poly(mul2(z, cap2));
-          float2 x = unpair(fma2(z, c2, off2));
+          float2 x = unpair(fma2(z, decltype(raw)::value ? poly.factor(z) : c2, off2));
           if (kPolyMask >> (i % 8) & 1)  // a masked score comes out as 2^-126
             x = exp2_poly(pair(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
           else
