@@ -349,11 +349,11 @@ rows_mma_kernel(const __grid_constant__ Args a) {
   // lane l (and l + 16) looks up token l of a step, one step before its loads
   auto page_of = [&](int step) -> int {
     const uint32_t u = (uint32_t)step * kStep + (lane & 15);
-    return step < last && (int)u < hi ? table[u / P] : -1;
+    return step < last && (int)u >= lo && (int)u < hi ? table[u / P] : -1;
   };
   auto issue = [&](int step, int page, int stage) -> uint32_t {
     const uint32_t u = (uint32_t)step * kStep + (lane & 15);
-    const bool in = step < last && (int)u < hi;
+    const bool in = step < last && (int)u >= lo && (int)u < hi;
     const bool ok = in && (uint32_t)page < pages;
     if (in && !ok && lane < 16) report(a.status, HKV_ERR_DEVICE_RANGE);
     const uint32_t row = ok ? ((uint32_t)page * a.Hkv + it.j) * P + u % P : 0xffffffffu;

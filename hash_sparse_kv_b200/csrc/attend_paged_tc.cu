@@ -248,67 +248,88 @@ __device__ __forceinline__ bool find_tile(const Args& a, int tile, int& b, int64
   }
 }
 
-// One tile of K or V into `dst` by a whole warp; true when TMA does it (the
-// barrier then completes by bytes, else lane 0 has arrived).  `valid` gets the
-// mask of tokens that were there.
-__device__ __forceinline__ void load_tile(const TcArgs& t, const void* pool, const CUtensorMap* map,
-                                          const int32_t* __restrict__ table, int u0, int n, int j, unsigned char* dst,
-                                          uint64_t* bar, uint4* valid) {
-  const Args& a = t.a;
-  const int lane = threadIdx.x & 31;
-  if (t.box > 0 && u0 + kTile <= n) {
-    const int boxes = kTile / t.box;  // at most 16
-    int64_t row = 0;
-    bool ok = true;
-    if (lane < boxes) {
-      row = pa::pool_row(a, table, u0 + lane * t.box, j);
-      ok = row >= 0;
-    }
-    if (__all_sync(0xffffffffu, ok)) {
-      if (lane == 0) {
-        if (valid) *valid = make_uint4(~0u, ~0u, ~0u, ~0u);
-        tc::mbar_expect_tx(bar, kBuf);
-      }
-      __syncwarp();
-      if (lane < boxes) {
-        tc::tma_load_2d(dst + lane * t.box * 128, map, 0, (int)row, bar);
-        tc::tma_load_2d(dst + kHalf + lane * t.box * 128, map, 64, (int)row, bar);
-      }
-      return;
+// The K or the V tiles of a CTA, brought in by one warp: by TMA where a tile is
+// whole and its pages are cut into boxes, else row by row with cp.async, whose
+// arrival this warp sees to one tile later (the tile before is complete while
+// this one is on its way).
+struct Loader {
+  const TcArgs& t;
+  const void* pool;
+  const CUtensorMap* map;
+  const int32_t* __restrict__ table;
+  int n_tok, j;              // tokens behind the table, KV head
+  int lo, hi;                // positions that some row sees: the places of others need not exist
+  int32_t rows[4];           // pool rows of tokens lane, lane + 32, + 64, + 96 of a tile, -1: none
+  uint64_t* pending = nullptr;  // the barrier of the tile whose copies have not been waited for
+
+  __device__ __forceinline__ void look(int n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = n * kTile + 32 * k + (threadIdx.x & 31);
+      rows[k] = u >= lo && u < hi ? (int32_t)pa::pool_row(t.a, table, u, j) : -1;
+      if (u >= lo && u < hi && rows[k] < 0) report(t.a.status, HKV_ERR_DEVICE_RANGE);
     }
   }
-  // plain loads: lane l finds the rows of tokens l, l + 32, l + 64, l + 96
-  int64_t rows[4];
-  uint32_t mask[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int u = u0 + 32 * k + lane;
-    rows[k] = u < n ? pa::pool_row(a, table, u, j) : -1;
-    if (u < n && rows[k] < 0) report(a.status, HKV_ERR_DEVICE_RANGE);
-    mask[k] = __ballot_sync(0xffffffffu, rows[k] >= 0);
+  // Copies of the pending tile have landed, but for the newest `kLater` groups.
+  template <int kLater>
+  __device__ __forceinline__ void settle() {
+    if (pending == nullptr) return;
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+    async_fence();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(pending);
+    pending = nullptr;
   }
-  if (valid && lane == 0) *valid = make_uint4(mask[0], mask[1], mask[2], mask[3]);
-  const int c = lane & 15;  // 16-byte piece of a row
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    for (int x0 = 0; x0 < 32; x0 += 16) {
-      uint4 v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t row = __shfl_sync(0xffffffffu, rows[k], x0 + 2 * e + (lane >> 4));
-        v[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (row >= 0) v[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(pool) + row * kHeadDim) + c);
+  // Tile n into `dst`; `bar` completes when it is there.  `valid` gets the mask
+  // of tokens that have a place.
+  __device__ __forceinline__ void load(int n, int end, unsigned char* dst, uint64_t* bar, uint4* valid) {
+    const int lane = threadIdx.x & 31;
+    if (t.box > 0) {
+      const int boxes = kTile / t.box;  // at most 16
+      int32_t row = 0;
+      bool ok = (n + 1) * kTile <= n_tok;
+      if (ok && lane < boxes) {
+        row = (int32_t)pa::pool_row(t.a, table, n * kTile + lane * t.box, j);
+        ok = row >= 0;
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int x = 32 * k + x0 + 2 * e + (lane >> 4);
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalf + x * 128 + (((c & 7) ^ (x & 7)) << 4)) = v[e];
+      if (__all_sync(0xffffffffu, ok)) {
+        settle<0>();
+        if (lane == 0) {
+          if (valid) *valid = make_uint4(~0u, ~0u, ~0u, ~0u);
+          tc::mbar_expect_tx(bar, kBuf);
+        }
+        __syncwarp();
+        if (lane < boxes) {
+          tc::tma_load_2d(dst + lane * t.box * 128, map, 0, row, bar);
+          tc::tma_load_2d(dst + kHalf + lane * t.box * 128, map, 64, row, bar);
+        }
+        return;
       }
+      look(n);
     }
-  async_fence();
-  __syncwarp();
-  if (lane == 0) tc::mbar_arrive(bar);
-}
+    uint32_t mask[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mask[k] = __ballot_sync(0xffffffffu, rows[k] >= 0);
+    if (valid && lane == 0) *valid = make_uint4(mask[0], mask[1], mask[2], mask[3]);
+    const int c = lane & 15;  // 16-byte piece of a row
+    const uint32_t to = tc::smem_u32(dst) + (c >> 3) * kHalf;
+    const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(pool) + c * 8;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll 4
+      for (int e = lane >> 4; e < 32; e += 2) {
+        const int32_t row = __shfl_sync(0xffffffffu, rows[k], e);
+        const int x = 32 * k + e;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + x * 128 + (((c & 7) ^ (x & 7)) << 4)),
+                     "l"(from + (row < 0 ? 0 : (int64_t)row * kHeadDim)), "r"(row < 0 ? 0 : 16)
+                     : "memory");
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    settle<1>();
+    pending = bar;
+    if (t.box == 0 && n + 1 < end) look(n + 1);
+  }
+};
 
 // A slot's tiles: every step-th from first up to last.
 struct Run {
@@ -429,15 +450,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       unsigned char* ring = smem + (is_k ? Layout::kK : Layout::kV);
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       if (t.box > 0 && lane == 0) tc::tma_prefetch_map(map);
+      Loader ld{t, is_k ? a.K : a.V, map, table, n_all, j, lo, hi, {-1, -1, -1, -1}};
+      if (t.box == 0 && t0 < t1) ld.look(t0);
       int stage = 0, armed = 0;
       uint32_t phase = 0;
       for (int n = t0; n < t1; ++n) {
-        if (!all(wait(&empty[stage], phase ^ 1u, abort, a.wait_ns))) break;
-        load_tile(t, is_k ? a.K : a.V, map, table, n * kTile, n_all, j, ring + stage * kBuf, &full[stage],
-                  is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
+        if (!all(tc::mbar_try_wait(&empty[stage], phase ^ 1u))) {
+          ld.settle<0>();  // what waits for the tile before may be what this one waits for
+          if (!all(wait(&empty[stage], phase ^ 1u, abort, a.wait_ns))) break;
+        }
+        ld.load(n, t1, ring + stage * kBuf, &full[stage], is_k ? &valid_s[(n - t0) % kMaskRing] : nullptr);
         ++armed;
         if (++stage == stages) stage = 0, phase ^= 1u;
       }
+      ld.settle<0>();
       // on an abort, let every load already issued land before the CTA leaves
       if (*abort && lane == 0)
         for (int n = max(0, armed - stages); n < armed; ++n) tc::mbar_drain(&full[n % stages], (n / stages) & 1, a.wait_ns);
