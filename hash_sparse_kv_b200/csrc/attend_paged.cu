@@ -263,20 +263,20 @@ rows_simt_kernel(const __grid_constant__ Args a) {
   finish<float, kPrefix>(a, it, q_s[0], m_s, l_s);
 }
 
-// ---- bf16: the same on the tensor cores of one warp --------------------------
-// Each of four warps takes every fourth step of 16 tokens with a ring of its
-// own (cp.async, three steps of 8 KB: 192 KB in flight on an SM with two
-// blocks), so nothing but the end of the block makes warps wait for each
-// other.  Scores and products are mma.sync m16n8k16 with the 16 rows as M: the
-// block is bound by reading K and V, and a 128-row tcgen05 tile would be seven
-// eighths padding.  P is rounded to bf16 for the product, sums stay fp32.
-constexpr int kMmaThreads = 128;
-constexpr int kMmaWarps = kMmaThreads / 32;
+// ---- bf16: a warp per item ---------------------------------------------------
+// An item is the up to 16 rows of one sequence and KV head and one run of
+// their positions.  A warp goes through items on its own: K and V arrive by
+// cp.async in steps of 16 tokens, three steps (24 KB) ahead, and the loads run
+// on into the warp's next item while this one is finished, so that the eight
+// warps of an SM keep 192 KB on their way without ever waiting for each other.
+// Scores and products are mma.sync m16n8k16 with the 16 rows as M: the work is
+// bound by reading K and V, and a 128-row tcgen05 tile would be seven eighths
+// padding.  P is rounded to bf16 for the product, sums stay fp32.
+constexpr int kWarps = 8;
 constexpr int kStep = 16;                    // tokens
 constexpr int kStages = 3;
 constexpr int kStepBytes = kStep * 256;      // of K, and again of V
-constexpr int kQPitch = kHeadDim + 8;
-constexpr size_t kMmaSmem = (size_t)kMmaWarps * kStages * 2 * kStepBytes;
+constexpr size_t kRingBytes = (size_t)kWarps * kStages * 2 * kStepBytes;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t p) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -297,68 +297,81 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kGeneral>
-__global__ void __launch_bounds__(kMmaThreads, 2)
-rows_mma_kernel(const __grid_constant__ Args a) {
-  constexpr int D = kHeadDim;
-  extern __shared__ __align__(128) unsigned char ring[];  // [warp][stage][K step, V step]; the parts in the end
-  __shared__ __align__(16) __nv_bfloat16 q_s[kRows][kQPitch];
-  __shared__ float m_s[kMmaWarps][kRows], l_s[kMmaWarps][kRows];
-  __shared__ int span_s[2];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Item it;
-  if (!item_of<false>(a, it)) return;
-  for (int i = tid; i < kRows * (D / 8); i += kMmaThreads) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (r < it.nrows)
-      v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + r / a.g) * a.q_stride +
-                                               (int64_t)(it.j * a.g + r % a.g) * D) + c);
-    *reinterpret_cast<uint4*>(&q_s[r][c * 8]) = v;
+// An item as every lane of its warp sees it; `mine` is what row `lane` sees.
+struct WarpItem {
+  int b, j, part, nrows;
+  int64_t row0;       // first new token among all
+  int lo, hi;         // positions that the rows see together
+  int first, last;    // the steps of this run
+  pa::Span mine;
+};
+__device__ __forceinline__ WarpItem open_item(const Args& a, int w, bool tell) {
+  const int lane = threadIdx.x & 31;
+  WarpItem it;
+  it.part = w % a.own_parts;
+  const int rest = w / a.own_parts;
+  it.j = rest % a.Hkv, it.b = rest / a.Hkv;
+  const pa::Seq s = pa::seq_of(a, it.b, tell && lane == 0 && it.part == 0 && it.j == 0);
+  it.row0 = s.first;
+  it.nrows = (int)s.n_new * a.g;
+  it.mine = pa::Span{0, INT32_MAX, 0};  // padding rows see everything: no masks for their sake
+  int lo = INT32_MAX, hi = 0;
+  if (lane < it.nrows) {
+    it.mine = pa::span_of(a, s, it.b, lane / a.g);
+    if (it.mine.lo < it.mine.hi) lo = it.mine.lo, hi = it.mine.hi;
   }
-  // this thread's two rows of every fragment; padding rows see everything
-  pa::Span sp[2];
-  float slope[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = lane / 4 + 8 * h;
-    sp[h] = r < it.nrows ? row_span<false>(a, it, r) : pa::Span{0, INT32_MAX, 0};
-    slope[h] = kGeneral && a.slopes && r < it.nrows ? a.slopes[it.j * a.g + r % a.g] * pa::kLog2e : 0.f;
-  }
-  if (warp == 0) {
-    int lo = INT32_MAX, hi = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (lane / 4 + 8 * h < it.nrows && sp[h].lo < sp[h].hi) lo = min(lo, sp[h].lo), hi = max(hi, sp[h].hi);
-    lo = __reduce_min_sync(0xffffffffu, lo), hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) span_s[0] = min(lo, hi), span_s[1] = hi;
-  }
-  __syncthreads();
-  const int lo = span_s[0], hi = span_s[1];
-  // this block's run of steps, aligned to steps of the sequence
-  const int s0 = lo / kStep, s1 = (hi + kStep - 1) / kStep, per = (s1 - s0 + gridDim.z - 1) / gridDim.z;
-  const int first = s0 + (int)blockIdx.z * per, last = hi > lo ? min(s1, first + per) : first;
-  uint32_t qf[8][4];
-#pragma unroll
-  for (int kk = 0; kk < 8; ++kk) ldsm4(qf[kk], sm32(&q_s[lane % 16][kk * 16 + lane / 16 * 8]));
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = min(__reduce_min_sync(0xffffffffu, lo), hi);
+  it.lo = lo, it.hi = hi;
+  const int s0 = lo / kStep, s1 = (hi + kStep - 1) / kStep, per = (s1 - s0 + a.own_parts - 1) / a.own_parts;
+  it.first = s0 + it.part * per;
+  it.last = hi > lo ? min(s1, it.first + per) : it.first;
+  return it;
+}
 
-  const int32_t* __restrict__ table = a.pm.table + (int64_t)it.b * a.pm.max_pages;
+template <bool kGeneral>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+rows_mma_kernel(const __grid_constant__ Args a, int items) {
+  constexpr int D = kHeadDim;
+  extern __shared__ __align__(1024) unsigned char ring[];  // [warp][stage][K step, V step]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the prefix's kernel may take the other SMs
+  const int worker = warp * gridDim.x + blockIdx.x, workers = gridDim.x * kWarps;
   const uint32_t P = a.pm.page_size, pages = (uint32_t)a.pm.num_pages;
   const uint32_t my_ring = sm32(ring) + warp * kStages * 2 * kStepBytes;
-  const __nv_bfloat16 *Kp = static_cast<const __nv_bfloat16*>(a.K), *Vp = static_cast<const __nv_bfloat16*>(a.V);
-  // lane l (and l + 16) looks up token l of a step, one step before its loads
-  auto page_of = [&](int step) -> int {
-    const uint32_t u = (uint32_t)step * kStep + (lane & 15);
-    return step < last && (int)u >= lo && (int)u < hi ? table[u / P] : -1;
+
+  // ---- where the loads are: item, step, and the page of this lane's token ----
+  // A step's tokens are brought two whole rows at a time (64 bytes of eight rows
+  // at a time took longer); piece c of token x lies at c ^ (x % 8).
+  int p_w = worker, p_step = 0, p_last = 0, p_lo = 0, p_hi = 0, p_j = 0, p_page = -1;
+  const int32_t* __restrict__ p_table = nullptr;
+  auto page_of = [&]() -> int {
+    const uint32_t u = (uint32_t)p_step * kStep + (lane & 15);
+    return p_step < p_last && (int)u >= p_lo && (int)u < p_hi ? p_table[u / P] : -1;
   };
-  auto issue = [&](int step, int page, int stage) -> uint32_t {
-    const uint32_t u = (uint32_t)step * kStep + (lane & 15);
-    const bool in = step < last && (int)u >= lo && (int)u < hi;
-    const bool ok = in && (uint32_t)page < pages;
-    if (in && !ok && lane < 16) report(a.status, HKV_ERR_DEVICE_RANGE);
-    const uint32_t row = ok ? ((uint32_t)page * a.Hkv + it.j) * P + u % P : 0xffffffffu;
-    if (step < last) {
-      const uint32_t base = my_ring + stage * 2 * kStepBytes;
+  auto open_loads = [&] {
+    const WarpItem it = open_item(a, p_w, true);
+    p_step = it.first, p_last = it.nrows > 0 ? it.last : it.first, p_lo = it.lo, p_hi = it.hi, p_j = it.j;
+    p_table = a.pm.table + (int64_t)it.b * a.pm.max_pages;
+    p_page = page_of();
+  };
+  // Bits 16 s ..: which tokens of the step loaded s steps ago have a place in
+  // the pool.
+  uint64_t there_of = 0;
+  int slot = 0;
+  auto load_next = [&] {
+    while (p_step >= p_last && p_w < items) {
+      p_w += workers;
+      if (p_w < items) open_loads();
+    }
+    bool ok = false;
+    if (p_w < items) {
+      const uint32_t u = (uint32_t)p_step * kStep + (lane & 15);
+      const bool in = (int)u >= p_lo && (int)u < p_hi;
+      ok = in && (uint32_t)p_page < pages;
+      if (in && !ok && lane < 16) report(a.status, HKV_ERR_DEVICE_RANGE);
+      const uint32_t row = ok ? ((uint32_t)p_page * a.Hkv + p_j) * P + u % P : 0xffffffffu;
+      const uint32_t base = my_ring + slot * 2 * kStepBytes;
       const int c = lane & 15;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -367,50 +380,82 @@ rows_mma_kernel(const __grid_constant__ Args a) {
         const uint32_t dst = base + x * 256 + ((c ^ (x & 7)) << 4);
         const int64_t off = rx == 0xffffffffu ? 0 : (int64_t)rx * D + c * 8;
         const int bytes = rx == 0xffffffffu ? 0 : 16;
-        cp16(dst, Kp + off, bytes);
-        cp16(dst + kStepBytes, Vp + off, bytes);
+        cp16(dst, static_cast<const __nv_bfloat16*>(a.K) + off, bytes);
+        cp16(dst + kStepBytes, static_cast<const __nv_bfloat16*>(a.V) + off, bytes);
       }
+      ++p_step;
+      p_page = page_of();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    return __ballot_sync(0xffffffffu, ok) & 0xffffu;
-  };
-
-  float acc[16][4] = {};
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
-  const float cap = a.softcap * pa::kLog2e;
-  // The loops over steps stay rolled: a block runs through few of them, and
-  // fetching unrolled code for the first time took longer than running it.
-  // Bits 16 s ..: which tokens of the step issued s steps ago have a place in
-  // the pool.
-  uint64_t there_of = 0;
-  int page = page_of(first + warp), ahead = first + warp, slot = 0;
-  auto issue_next = [&] {
-    const int next = page_of(ahead + kMmaWarps);
-    there_of = there_of << 16 | issue(ahead, page, slot);
-    page = next;
-    ahead += kMmaWarps;
+    there_of = there_of << 16 | (__ballot_sync(0xffffffffu, ok) & 0xffffu);
     if (++slot == kStages) slot = 0;
   };
+  // The first lines that an item needs, the start of its page table and its
+  // queries, are called into L2 while the warp's item before it is worked on.
+  auto call_in = [&](int w) {
+    if (w >= items) return;
+    const int rest = w / a.own_parts, j = rest % a.Hkv, b = rest / a.Hkv;
+    const int64_t tok = a.cu ? a.cu[b] : b;
+    const void* at = lane == 0 ? static_cast<const void*>(a.pm.table + (int64_t)b * a.pm.max_pages)
+                               : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride + (int64_t)j * a.g * D + (lane - 1) * 64;
+    if (lane <= 2 * a.g && (lane == 0 || tok < a.T)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+  };
+  call_in(worker);
+  call_in(worker + workers);
+  if (p_w < items) open_loads();
 #pragma unroll 1
-  for (int s = 0; s < kStages; ++s) issue_next();
-  {
+  for (int s = 0; s < kStages - 1; ++s) load_next();
+
+  const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
+  const float cap = a.softcap * pa::kLog2e;
+  const int parts = a.prefix_parts + a.own_parts;
 #pragma unroll 1
-    for (int step = first + warp; step < last; step += kMmaWarps) {
-      const uint32_t there = (uint32_t)(there_of >> (16 * (kStages - 1))) & 0xffffu;
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  for (int w = worker; w < items; w += workers) {
+    call_in(w + 2 * workers);
+    const WarpItem it = open_item(a, w, false);
+    if (it.nrows == 0) continue;
+    // this thread's two rows of every fragment, and the queries of them: A
+    // fragments straight from memory
+    pa::Span sp[2];
+    float slope[2];
+    uint32_t qf[8][4];
+    int64_t row_at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = lane / 4 + 8 * h;
+      sp[h] = pa::Span{__shfl_sync(0xffffffffu, it.mine.lo, r), __shfl_sync(0xffffffffu, it.mine.hi, r),
+                       __shfl_sync(0xffffffffu, it.mine.pos, r)};
+      const int head = it.j * a.g + r % a.g;
+      slope[h] = kGeneral && a.slopes && r < it.nrows ? a.slopes[head] * pa::kLog2e : 0.f;
+      row_at[h] = (it.row0 + r / a.g) * a.Hq + head;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + r / a.g) * a.q_stride +
+                                                            (int64_t)head * D) + lane % 4;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        qf[kk][h] = r < it.nrows ? __ldg(q + kk * 8) : 0u;
+        qf[kk][2 + h] = r < it.nrows ? __ldg(q + kk * 8 + 4) : 0u;
+      }
+    }
+    float acc[16][4] = {};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll 1
+    for (int step = it.first; step < it.last; ++step) {
+      const uint32_t there = (uint32_t)(there_of >> (16 * (kStages - 2))) & 0xffffu;
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
-      const uint32_t kb = my_ring + slot * 2 * kStepBytes, vb = kb + kStepBytes;
-      float z[2][4] = {};
+      // `slot` is the next one to fill, which the last step left: this step's is one on
+      const uint32_t kb = my_ring + (slot + 1 == kStages ? 0 : slot + 1) * 2 * kStepBytes, vb = kb + kStepBytes;
+      float z[2][4] = {}, y[2][4] = {};  // even and odd kk: half as long a chain of MMAs
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         // tokens 0-7 and 8-15 of the step, elements kk * 16 + 0-7 and 8-15
         uint32_t b[4];
         const int x = (lane & 7) + (lane >> 4) * 8, ch = kk * 2 + ((lane >> 3) & 1);
         ldsm4(b, kb + x * 256 + ((ch ^ (x & 7)) << 4));
-        mma16816(z[0], qf[kk], b[0], b[1]);
-        mma16816(z[1], qf[kk], b[2], b[3]);
+        mma16816(kk & 1 ? y[0] : z[0], qf[kk], b[0], b[1]);
+        mma16816(kk & 1 ? y[1] : z[1], qf[kk], b[2], b[3]);
       }
+      load_next();  // here, where the scores are not there yet
       const int u0 = step * kStep + (lane & 3) * 2;  // this thread's tokens: u0, u0 + 1, u0 + 8, u0 + 9
       float top[2] = {-INFINITY, -INFINITY};
       const bool whole = there == 0xffffu && sp[0].lo <= step * kStep && sp[1].lo <= step * kStep &&
@@ -420,7 +465,7 @@ rows_mma_kernel(const __grid_constant__ Args a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = e >> 1, u = u0 + n * 8 + (e & 1);
-          float x = z[n][e] * zs;
+          float x = (z[n][e] + y[n][e]) * zs;
           if (kGeneral) {
             if (cap > 0.f) x = pa::capped(x, cap);
             x = fmaf(-slope[h], fabsf((float)(sp[h].pos - u)), x);
@@ -464,50 +509,29 @@ rows_mma_kernel(const __grid_constant__ Args a) {
         mma16816(acc[2 * d + 1], pf, b[2], b[3]);
       }
       __syncwarp();
-      issue_next();
+    }
+    // this run's part, or the finished rows
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (lane / 4 + 8 * h >= it.nrows) continue;
+      if (parts > 1) {
+        const int64_t row = (a.prefix_parts + it.part) * a.T * a.Hq + row_at[h];
+        if ((lane & 3) == 0) a.part_ml[row] = make_float2(m[h], l[h]);
+        float2* dst = reinterpret_cast<float2*>(a.part_o + row * D) + (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[i * 4] = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+      } else {
+        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+        if ((lane & 3) == 0 && a.lse) a.lse[row_at[h]] = l[h] > 0.f ? (m[h] + log2f(l[h])) * pa::kLn2 : -INFINITY;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row_at[h] * D) + (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[i * 4] = pack2(acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
+      }
     }
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    if ((lane & 3) == 0) m_s[warp][lane / 4 + 8 * h] = m[h], l_s[warp][lane / 4 + 8 * h] = l[h];
-  }
-  __syncthreads();  // every warp's loads have landed and been used: the ring is free
-  // the four warps' results join in shared memory
-  float* o_w = reinterpret_cast<float*>(ring);  // [warp][row][column]
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      *reinterpret_cast<float2*>(&o_w[(warp * kRows + lane / 4 + 8 * h) * D + i * 8 + (lane & 3) * 2]) =
-          make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
-  __syncthreads();
-  __shared__ float mm[kRows], ll[kRows], fw[kMmaWarps][kRows];
-  if (tid < kRows) {
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMmaWarps; ++w) M = fmaxf(M, m_s[w][tid]);
-#pragma unroll
-    for (int w = 0; w < kMmaWarps; ++w) {
-      fw[w][tid] = m_s[w][tid] == -INFINITY ? 0.f : exp2f(m_s[w][tid] - M);
-      L = fmaf(fw[w][tid], l_s[w][tid], L);
-    }
-    mm[tid] = M, ll[tid] = L;
-  }
-  __syncthreads();
-  for (int i = tid; i < it.nrows * D; i += kMmaThreads) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMmaWarps; ++w) x = fmaf(fw[w][i / D], o_w[w * kRows * D + i], x);
-    o_w[i] = x;
-  }
-  __syncthreads();
-  finish<__nv_bfloat16, false>(a, it, o_w, mm, ll);
-  // launched while the prefix's kernel may still run: whatever waits for this
-  // grid waits for that one too
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Joins the parts of every row: out = sum_p 2^(m_p - M) o_p / L, with M the
@@ -561,31 +585,16 @@ join_parts_kernel(const __grid_constant__ Args a) {
   if (lane == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
 }
 
-// Launches a kernel that may be scheduled while the one before it on the stream
-// still runs (it waits for that one itself).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t c{};
-  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &at, c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
-// Runs of positions that an item's blocks take: few items are cut until two
-// blocks per SM are there, down to 128 tokens; many items only into runs of at
-// least 2048 tokens, eight blocks per SM, so that the last ones to run are
-// short (64 sequences of up to 8192 tokens: 306 us whole, 277 us in runs of
-// 2730).
-int splits_for(int64_t items, int64_t tokens) {
-  const int64_t sms = sm_count();
-  auto cut = [&](int64_t per_sm, int64_t least) {
-    const int64_t want = ceil_div(per_sm * sms, items < 1 ? 1 : items), most = ceil_div(tokens, least);
+// Runs of positions that an item is cut into.  Few items are cut until every
+// worker has one, down to 128 tokens; many items only into runs of at least
+// 512 tokens, six for every worker, so that the last ones to run are short.
+int splits_for(int64_t items, int64_t tokens, int64_t workers) {
+  auto cut = [&](int64_t want, int64_t least) {
+    want = ceil_div(want, items < 1 ? 1 : items);
+    const int64_t most = ceil_div(tokens, least);
     return want < most ? want : most;
   };
-  const int64_t few = cut(2, 128), many = cut(8, 2048), s = few > many ? few : many;
+  const int64_t few = cut(workers, 128), many = cut(6 * workers, 512), s = few > many ? few : many;
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
@@ -593,29 +602,44 @@ int splits_for(int64_t items, int64_t tokens) {
 // workspace can be sized before the call.
 struct Plan {
   bool tc = false;         // prompts: the tensor-core kernel takes all rows
-  bool tc_prefix = false;  // it takes the shared prefix
-  int64_t own_items = 0;
+  int64_t own_items = 0;   // rows of one sequence (16 at most), all KV heads together
   int prefix_parts = 0, own_parts = 1;
-  int parts = 0;          // a row's partial results, 0 when its block finishes it
+  int row_ctas = 0;        // bf16: blocks of the single-token kernel, one per SM
+  int parts = 0;           // a row's partial results, 0 when its block finishes it
   size_t o = 0, total = 0;  // byte offset of part_o behind part_ml, and the size
 };
 
 Plan plan(const PagedAttend& p) {
   Plan r;
-  const int g = p.Hq / p.Hkv, tpt = kRows / g;
+  const int g = p.Hq / p.Hkv, tpt = kRows / g, sms = sm_count();
   const bool bf16 = p.dtype == HKV_BF16;
   // a sequence's new tokens fill more than the 16 rows of one block: 128-row tiles
   r.tc = bf16 && p.cu_q_rows && (int64_t)p.max_q * g > kRows;
   if (r.tc) {
-    r.own_parts = tc_splits(p, false);
+    r.own_parts = tc_splits(p, false, sms);
   } else {
-    r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt);
-    r.own_parts = splits_for(r.own_items * p.Hkv, p.n_max);
-    r.tc_prefix = bf16 && p.n_prefix > 0;
-    if (r.tc_prefix)
-      r.prefix_parts = tc_splits(p, true);
-    else if (p.n_prefix > 0)
-      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix);
+    r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt) * p.Hkv;
+    // two fp32 blocks, or eight bf16 warps, per SM
+    r.own_parts = splits_for(r.own_items, p.n_max, (bf16 ? kWarps : 2) * sms);
+    const int64_t items = r.own_items * r.own_parts;
+    r.row_ctas = (int)(items < sms ? items : sms);
+    if (p.n_prefix > 0 && bf16) {
+      // The prefix (bound by the tensor cores) and the sequences' own tokens
+      // (bound by memory) run side by side on SMs of their own, shared out by
+      // the time that each would take of one SM: 1.75 us for a tile of 128
+      // tokens and 256 rows, 45 GB/s and 0.5 us an item for the own tokens,
+      // taken to be half as long as they may be.  (64 sequences of up to 512
+      // tokens behind 32768: one after the other 73 us, side by side 63 us; 256
+      // of up to 128 behind 98304: 409 and 375 us.)
+      const double prefix_us = 1.75 * (double)tc_tiles(p, true) * p.Hkv * (double)ceil_div(p.n_prefix, 128);
+      const double own_us = (double)p.B * p.Hkv * (double)p.n_max * 0.5 * 512 / 45e3 + 0.5 * (double)items;
+      const int share = (int)(sms * own_us / (own_us + prefix_us) + 0.5);
+      r.row_ctas = share < 1 ? 1 : share > sms - sms / 8 ? sms - sms / 8 : share;
+      if (r.row_ctas > items) r.row_ctas = (int)items;
+      r.prefix_parts = tc_splits(p, true, sms - r.row_ctas);
+    } else if (p.n_prefix > 0) {
+      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix, 2 * sms);
+    }
   }
   r.parts = r.prefix_parts > 0 || r.own_parts > 1 ? r.prefix_parts + r.own_parts : 0;
   r.o = align_up(sizeof(float2) * r.parts * p.T * p.Hq, 256);
@@ -623,44 +647,37 @@ Plan plan(const PagedAttend& p) {
   return r;
 }
 
-template <typename T>
-int run(const PagedAttend& p, const Plan& pl, Args& a, cudaStream_t st) {
-  int rc = HKV_OK;
-  if (pl.tc) {
-    rc = launch_attend_tc(p, a, false, pl.own_parts, pl.parts ? 0 : -1, st);
-  } else {
-    if (pl.prefix_parts > 0) {
-      if constexpr (sizeof(T) == 4) {
-        rc = cuda_check(cudaFuncSetAttribute(rows_simt_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)(kSimtStages * sizeof(SimtStage))), "prefix attention smem attribute");
-        if (rc != HKV_OK) return rc;
-        rows_simt_kernel<true><<<dim3((unsigned)ceil_div(p.B, kRows / a.g), p.Hkv, pl.prefix_parts), kThreads,
-                                 kSimtStages * sizeof(SimtStage), st>>>(a);
-        rc = cuda_check(cudaGetLastError(), "prefix attention launch");
-      } else {
-        rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
-      }
-      if (rc != HKV_OK) return rc;
-    }
-    const dim3 grid((unsigned)pl.own_items, p.Hkv, pl.own_parts);
-    if constexpr (sizeof(T) == 2) {
-      auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMmaSmem);
-      if (e == cudaSuccess) {
-        if (pl.prefix_parts > 0)  // beside the prefix's kernel, which it does not depend on
-          e = launch_after(kernel, grid, kMmaThreads, kMmaSmem, st, a);
-        else
-          kernel<<<grid, kMmaThreads, kMmaSmem, st>>>(a), e = cudaGetLastError();
-      }
-      rc = cuda_check(e, "paged attention launch");
-    } else {
-      rc = cuda_check(cudaFuncSetAttribute(rows_simt_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)(kSimtStages * sizeof(SimtStage))), "paged attention smem attribute");
-      if (rc != HKV_OK) return rc;
-      rows_simt_kernel<false><<<grid, kThreads, kSimtStages * sizeof(SimtStage), st>>>(a);
-      rc = cuda_check(cudaGetLastError(), "paged attention launch");
-    }
+int run_fp32(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
+  constexpr size_t smem = kSimtStages * sizeof(SimtStage);
+  for (int prefix = pl.prefix_parts > 0; prefix >= 0; --prefix) {
+    auto kernel = prefix ? rows_simt_kernel<true> : rows_simt_kernel<false>;
+    const int rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
+                              "paged attention smem attribute");
+    if (rc != HKV_OK) return rc;
+    const int64_t blocks = prefix ? ceil_div(p.B, kRows / a.g) : pl.own_items / p.Hkv;
+    kernel<<<dim3((unsigned)blocks, p.Hkv, prefix ? pl.prefix_parts : pl.own_parts), kThreads, smem, st>>>(a);
+    const int rc2 = cuda_check(cudaGetLastError(), "paged attention launch");
+    if (rc2 != HKV_OK) return rc2;
   }
+  return HKV_OK;
+}
+
+int run_bf16(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
+  if (pl.tc) return launch_attend_tc(p, a, false, pl.own_parts, pl.parts ? 0 : -1, st);
+  const int64_t items = pl.own_items * pl.own_parts;
+  if (items > INT32_MAX / 2) return fail(HKV_ERR_UNSUPPORTED, "too many sequences and heads");
+  auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
+  int rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes),
+                      "paged attention smem attribute");
+  if (rc != HKV_OK) return rc;
+  kernel<<<pl.row_ctas, kWarps * 32, kRingBytes, st>>>(a, (int)items);
+  rc = cuda_check(cudaGetLastError(), "paged attention launch");
+  return rc == HKV_OK && pl.prefix_parts > 0 ? launch_attend_tc(p, a, true, pl.prefix_parts, 0, st) : rc;
+}
+
+template <typename T>
+int run(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
+  const int rc = sizeof(T) == 2 ? run_bf16(p, pl, a, st) : run_fp32(p, pl, a, st);
   if (rc != HKV_OK || pl.parts == 0) return rc;
   return cuda_check(launch_after(join_parts_kernel<T>, dim3((unsigned)ceil_div(a.T * a.Hq, 4)), 128, 0, st, a),
                     "attention join launch");

@@ -134,9 +134,22 @@ __device__ __forceinline__ int find_seq(const int32_t* __restrict__ cu, int B, i
 
 }  // namespace pa
 
+// Launches a kernel that may be scheduled while the one before it on the stream
+// still runs (it waits for that one itself).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at, c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 // The tensor-core kernel (attend_paged_tc.cu): row tiles, splits, launch.
 int64_t tc_tiles(const PagedAttend& p, bool prefix);
-int tc_splits(const PagedAttend& p, bool prefix);
+int tc_splits(const PagedAttend& p, bool prefix, int sms);
 int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int splits, int part0, cudaStream_t st);
 
 }  // namespace hkv

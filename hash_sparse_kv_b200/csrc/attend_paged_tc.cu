@@ -832,6 +832,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     tc::fence_after_sync();
     tc::tmem_free(tmem, 512);
   }
+  // launched while the own tokens' kernel may still run: whatever waits for
+  // this grid waits for that one too
+  if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -873,14 +876,28 @@ int64_t tc_tiles(const PagedAttend& p, bool prefix) {
   return prefix ? ceil_div(rows, 2 * kTile) : rows / (2 * kTile) + (p.B < p.T ? p.B : p.T);
 }
 
-// One wave of CTAs where the rows alone leave SMs idle, each with at least
-// two tiles of positions (with at most 128 rows, one for each slot).
-int tc_splits(const PagedAttend& p, bool prefix) {
-  const int64_t ctas = tc_tiles(p, prefix) * p.Hkv, sms = sm_count();
-  const int64_t most = ceil_div(prefix ? p.n_prefix : p.n_max, 2 * kTile);
-  int64_t s = sms / (ctas < 1 ? 1 : ctas);
-  s = s < most ? s : most;
-  return (int)(s < 1 ? 1 : s);
+// Runs that the positions are cut into.  A prefix is cut to take the least time
+// on `sms` SMs: whole waves of CTAs, each 7.5 us and 1.75 us for a tile of 128
+// tokens (half of it where a CTA's two slots take turns), and the joining of
+// parts at 4 TB/s.  Prompts, whose rows mostly see different lengths, are cut
+// only where they leave SMs idle, down to two tiles.
+int tc_splits(const PagedAttend& p, bool prefix, int sms) {
+  const int64_t ctas = tc_tiles(p, prefix) * p.Hkv;
+  if (!prefix) {
+    const int64_t most = ceil_div(p.n_max, 2 * kTile);
+    int64_t s = sms / (ctas < 1 ? 1 : ctas);
+    s = s < most ? s : most;
+    return (int)(s < 1 ? 1 : s);
+  }
+  const int64_t tiles = ceil_div(p.n_prefix, kTile);
+  const double tile_us = p.T * (p.Hq / p.Hkv) > kTile ? 1.75 : 0.9, part_us = (double)p.T * p.Hq * 512 / 4e6;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= 64 && s <= tiles; ++s) {
+    const double t = (double)ceil_div(ctas * s, sms) * ((double)ceil_div(tiles, s) * tile_us + 7.5) + s * part_us;
+    if (t < least) least = t, best = s;
+  }
+  return best;
 }
 
 int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int splits, int part0, cudaStream_t st) {
@@ -905,8 +922,9 @@ int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int s
   if (e != cudaSuccess) return cuda_check(e, "attention smem attribute");
   const int64_t grid = (int64_t)t.tiles * splits * p.Hkv;
   if (grid > INT32_MAX) return fail(HKV_ERR_UNSUPPORTED, "too many row tiles (%lld)", (long long)grid);
-  kernel<<<(unsigned)grid, kThreads, kSmem, st>>>(kmap, vmap, t);
-  return cuda_check(cudaGetLastError(), "attention launch");
+  if (prefix) e = launch_after(kernel, dim3((unsigned)grid), kThreads, kSmem, st, kmap, vmap, t);  // beside the own tokens' kernel
+  else kernel<<<(unsigned)grid, kThreads, kSmem, st>>>(kmap, vmap, t), e = cudaGetLastError();
+  return cuda_check(e, "attention launch");
 }
 
 }  // namespace hkv
