@@ -1,13 +1,24 @@
 // Dense attention over a paged cache for few rows at a time: the single-token
 // (decode) form of the prompt attention, the own tokens of sequences behind a
-// shared prefix, and fp32 caches.
+// shared prefix, and everything in fp32.
 //
-// A block takes the rows of up to 16 / g new tokens of one KV head (g query
-// heads a token share its keys) and one run of their cache positions, reads
-// that run once, and keeps the softmax's running maximum and sum and the
-// weighted values in registers (fp32).  Where few blocks would be left, the
-// positions are split over several blocks and a second launch joins their
-// partial results.
+// An item is up to 16 rows of one KV head (the g query heads of 16 / g new
+// tokens) and one run of their cache positions.  A warp goes through items on
+// its own, reads each run once and keeps the softmax's running maximum and sum
+// and the weighted values in registers (fp32).  Where few items would be left,
+// the positions are cut into more runs and a second launch joins their partial
+// results.
+//
+// K and V arrive by cp.async in steps of 8 KB (16 tokens in bf16, 8 in fp32),
+// two steps ahead, and the loads run on into the warp's next item while this
+// one is finished, so that the eight warps of an SM keep 128 KB on their way
+// without ever waiting for each other.  The work is bound by reading K and V: a
+// 128-row tcgen05 tile would be seven eighths padding, so scores and products
+// are mma.sync with the 16 rows as M.
+//   bf16: m16n8k16; P is rounded to bf16 for the product, sums stay fp32.
+//   fp32: m16n8k8 tf32 in three products.  x = hi + lo with hi the upper 19
+//         bits of x; hi hi + hi lo + lo hi leaves out lo lo and what tf32 drops
+//         of lo, 2^-21 of a product, beside fp32's own 2^-24 for each of 128.
 #include <cstdio>
 
 #include "attend_paged.cuh"
@@ -17,9 +28,7 @@ namespace {
 
 using pa::Args;
 
-constexpr int kThreads = 256;
 constexpr int kRows = 16;
-constexpr int kTile = 32;
 
 __device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
 __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
@@ -27,255 +36,15 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Which rows a block has and which positions of which table they see.
-struct Item {
-  int b, j, nrows;
-  int64_t i0, row0;  // first new token within its sequence, and among all
-  pa::Seq s;
-};
-
-template <bool kPrefix>
-__device__ __forceinline__ bool item_of(const Args& a, Item& it) {
-  const int tpt = kRows / a.g;  // tokens per block
-  it.j = blockIdx.y;
-  if constexpr (kPrefix) {  // rows of all sequences side by side
-    it.b = 0, it.i0 = (int64_t)blockIdx.x * tpt, it.row0 = it.i0;
-    it.s = pa::Seq{0, a.T, 0};
-  } else {
-    const int tiles = (a.max_q + tpt - 1) / tpt;
-    it.b = blockIdx.x / tiles, it.i0 = (int64_t)(blockIdx.x % tiles) * tpt;
-    it.s = pa::seq_of(a, it.b, it.i0 == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0);
-    it.row0 = it.s.first + it.i0;
-  }
-  if (it.i0 >= it.s.n_new) return false;
-  it.nrows = (int)min((int64_t)tpt, it.s.n_new - it.i0) * a.g;
-  return true;
-}
-
-// What row r of the item sees; positions count from the start of its table.
-template <bool kPrefix>
-__device__ __forceinline__ pa::Span row_span(const Args& a, const Item& it, int r) {
-  const int64_t i = it.i0 + r / a.g;
-  if constexpr (kPrefix) {
-    const int64_t n = min((int64_t)max(a.n_tok[i], 0), a.n_max);
-    return pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
-  } else {
-    return pa::span_of(a, it.s, it.b, i);
-  }
-}
-
-__device__ __forceinline__ int64_t out_row(const Args& a, const Item& it, int r) {
-  return (it.row0 + r / a.g) * a.Hq + it.j * a.g + r % a.g;
-}
-
-// The block's result: maximum, sum and weighted values of its rows, in shared
-// memory (o_s [kRows][kHeadDim], m_s and l_s [kRows]).  Every thread of the block
-// comes here after a barrier.
-template <typename T, bool kPrefix>
-__device__ void finish(const Args& a, const Item& it, const float* o_s, const float* m_s, const float* l_s) {
-  constexpr int Q = kHeadDim / 4;  // float4 pieces of a row
-  const int parts = a.prefix_parts + a.own_parts;
-  for (int i = threadIdx.x; i < it.nrows * Q; i += blockDim.x) {
-    const int r = i / Q;
-    int64_t row = out_row(a, it, r);
-    float4 x = reinterpret_cast<const float4*>(o_s)[i];
-    if (parts > 1) {
-      row += (kPrefix ? blockIdx.z : a.prefix_parts + blockIdx.z) * a.T * a.Hq;
-      reinterpret_cast<float4*>(a.part_o)[row * Q + i % Q] = x;
-      if (i % Q == 0) a.part_ml[row] = make_float2(m_s[r], l_s[r]);
-    } else {
-      const float inv = l_s[r] > 0.f ? 1.f / l_s[r] : 0.f;
-      x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      put4(static_cast<T*>(a.out) + row * kHeadDim + i % Q * 4, x);
-      if (i % Q == 0 && a.lse) a.lse[row] = l_s[r] > 0.f ? (m_s[r] + log2f(l_s[r])) * pa::kLn2 : -INFINITY;
-    }
-  }
-}
-
 __device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-
-// fp32: eight warps, tiles of 32 tokens staged in shared memory (cp.async, two
-// tiles ahead, their places looked up one tile before that).  A warp has two rows to itself: lane u scores
-// them against token u, then holds four output columns of each, so that only
-// the staging makes warps wait for each other.  Bound by the shared memory
-// reads of the two products; two rows a warp and 16-byte reads keep them at
-// three for 16 multiply-adds, which go two to an instruction.
-constexpr int kSimtStages = 3, kSimtKPitch = kHeadDim + 4;
-struct SimtStage {
-  float k[kTile][kSimtKPitch];
-  float v[kTile][kHeadDim];
-  bool there[kTile];
-};
-
-template <bool kPrefix>
-__global__ void __launch_bounds__(kThreads, 2)
-rows_simt_kernel(const __grid_constant__ Args a) {
-  constexpr int D = kHeadDim;
-  static_assert(kRows == 2 * (kThreads / 32) && kTile == 32, "two rows a warp, a token a lane");
-  __shared__ __align__(16) float q_s[kRows][D];  // the block's result in the end
-  __shared__ __align__(16) float p_s[kRows][kTile];
-  __shared__ float m_s[kRows], l_s[kRows];
-  extern __shared__ __align__(16) unsigned char simt_smem[];
-  SimtStage* const stages = reinterpret_cast<SimtStage*>(simt_smem);
-  __shared__ int lo_s, hi_s;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Item it;
-  if (!item_of<kPrefix>(a, it)) return;
-  if (tid == 0) lo_s = INT32_MAX, hi_s = 0;
-  pa::Span sp[2];
-  float slope[2];
-  const int r0 = warp * 2;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = r0 + h;
-    const float* q = static_cast<const float*>(a.q) + (it.row0 + r / a.g) * a.q_stride + (int64_t)(it.j * a.g + r % a.g) * D;
-    *reinterpret_cast<float4*>(&q_s[r][lane * 4]) =
-        r < it.nrows ? __ldg(reinterpret_cast<const float4*>(q) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    sp[h] = r < it.nrows ? row_span<kPrefix>(a, it, r) : pa::Span{0, 0, 0};
-    slope[h] = a.slopes && r < it.nrows ? a.slopes[it.j * a.g + r % a.g] * pa::kLog2e : 0.f;
-  }
-  __syncthreads();
-  if (lane < 2) {
-    const pa::Span x = lane ? sp[1] : sp[0];
-    if (x.lo < x.hi) {
-      atomicMin(&lo_s, x.lo);
-      atomicMax(&hi_s, x.hi);
-    }
-  }
-  __syncthreads();
-  const int lo = min(lo_s, hi_s), hi = hi_s;
-  const int tiles = (hi - lo + kTile - 1) / kTile, per = (tiles + gridDim.z - 1) / gridDim.z;
-  const int t0 = blockIdx.z * per, t1 = min(tiles, t0 + per);
-  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)it.b * a.pm.max_pages;
-  // this thread moves piece tid % 32 of tokens tid / 32 + 8 k
-  const int x0 = tid / 32, piece = tid % 32 * 4;
-  // lane u looks up token u of a tile
-  auto row_at = [&](int t) -> int64_t {
-    const int at = lo + t * kTile + lane;
-    if (t >= t1 || at >= hi) return -1;
-    const int64_t row = pa::pool_row(a, table, at, it.j);
-    if (row < 0) report(a.status, HKV_ERR_DEVICE_RANGE);
-    return row;
-  };
-  int64_t row = row_at(t0);
-  int ahead = t0, to = 0;
-  auto fetch_next = [&] {
-    if (ahead < t1) {
-      SimtStage& st = stages[to];
-      if (warp == 0) st.there[lane] = row >= 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t from = __shfl_sync(0xffffffffu, row, x0 + 8 * k);
-        const int64_t off = from >= 0 ? from * D + piece : 0;
-        cp16(sm32(&st.k[x0 + 8 * k][piece]), static_cast<const float*>(a.K) + off, from >= 0 ? 16 : 0);
-        cp16(sm32(&st.v[x0 + 8 * k][piece]), static_cast<const float*>(a.V) + off, from >= 0 ? 16 : 0);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    row = row_at(++ahead);
-    if (++to == kSimtStages) to = 0;
-  };
-  uint64_t acc[2][2] = {};  // rows r0 and r0 + 1, columns 4 lane .. 4 lane + 3
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll 1
-  for (int k = 0; k < kSimtStages - 1; ++k) fetch_next();
-  int at = 0;
-  for (int t = t0; t < t1; ++t) {
-    const int pos = lo + t * kTile + lane;
-    const SimtStage& st = stages[at];
-    if (++at == kSimtStages) at = 0;
-    asm volatile("cp.async.wait_group %0;" ::"n"(kSimtStages - 2) : "memory");
-    __syncthreads();  // this tile is there; the one before it has been used
-    fetch_next();
-    uint64_t z2[2][2] = {};
-#pragma unroll 4
-    for (int d = 0; d < D; d += 4) {
-      const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&st.k[lane][d]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&q_s[r0 + h][d]);
-        z2[h][0] = fma2(q.x, k.x, z2[h][0]);
-        z2[h][1] = fma2(q.y, k.y, z2[h][1]);
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float2 x = unpair(z2[h][0]), y = unpair(z2[h][1]);
-      float s = ((x.x + x.y) + (y.x + y.y)) * a.scale;
-      if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-      s = s * pa::kLog2e - slope[h] * (float)abs(sp[h].pos - pos);
-      if (pos < sp[h].lo || pos >= sp[h].hi || !st.there[lane]) s = -INFINITY;
-      float top = s;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mn = fmaxf(m[h], top), use = mn == -INFINITY ? 0.f : mn;
-      const float p = exp2f(s - use), f = exp2f(m[h] - use);
-      p_s[r0 + h][lane] = p;
-      l[h] = l[h] * f + p;  // this lane's tokens; the lanes' sums meet in the end
-      m[h] = mn;
-      const uint64_t f2 = pair(f, f);
-      acc[h][0] = fma2(acc[h][0], f2, 0), acc[h][1] = fma2(acc[h][1], f2, 0);
-    }
-    __syncwarp();
-#pragma unroll 1
-    for (int x = 0; x < kTile; x += 4) {
-      const float4 pa4 = *reinterpret_cast<const float4*>(&p_s[r0][x]), pb4 = *reinterpret_cast<const float4*>(&p_s[r0 + 1][x]);
-      const float pr[2][4] = {{pa4.x, pa4.y, pa4.z, pa4.w}, {pb4.x, pb4.y, pb4.z, pb4.w}};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&st.v[x + e][lane * 4]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t p2 = pair(pr[h][e], pr[h][e]);
-          acc[h][0] = fma2(p2, v.x, acc[h][0]);
-          acc[h][1] = fma2(p2, v.y, acc[h][1]);
-        }
-      }
-    }
-    __syncwarp();
-  }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-    *reinterpret_cast<ulonglong2*>(&q_s[r0 + h][lane * 4]) = make_ulonglong2(acc[h][0], acc[h][1]);  // this warp's own rows
-    if (lane == 0) m_s[r0 + h] = m[h], l_s[r0 + h] = l[h];
-  }
-  __syncthreads();
-  finish<float, kPrefix>(a, it, q_s[0], m_s, l_s);
-}
-
-// ---- bf16: a warp per item ---------------------------------------------------
-// An item is the up to 16 rows of one sequence and KV head and one run of
-// their positions.  A warp goes through items on its own: K and V arrive by
-// cp.async in steps of 16 tokens, three steps (24 KB) ahead, and the loads run
-// on into the warp's next item while this one is finished, so that the eight
-// warps of an SM keep 192 KB on their way without ever waiting for each other.
-// Scores and products are mma.sync m16n8k16 with the 16 rows as M: the work is
-// bound by reading K and V, and a 128-row tcgen05 tile would be seven eighths
-// padding.  P is rounded to bf16 for the product, sums stay fp32.
 constexpr int kWarps = 8;
-constexpr int kStep = 16;                    // tokens
 constexpr int kStages = 3;
-constexpr int kStepBytes = kStep * 256;      // of K, and again of V
+constexpr int kStepBytes = 4096;             // of K, and again of V
+template <typename T>
+constexpr int kStep = kStepBytes / (kHeadDim * (int)sizeof(T));  // tokens: 16 or 8
 constexpr size_t kRingBytes = (size_t)kWarps * kStages * 2 * kStepBytes;
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t p) {
@@ -292,67 +61,124 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// d += a b for fp32 a (16 x 8) and b (8 x 8).
+__device__ __forceinline__ void mma_fp32(float (&d)[4], const float (&a)[4], float b0, float b1) {
+  uint32_t ah[4], al[4], bh[2], bl[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_tf32(a[i], ah[i], al[i]);
+  split_tf32(b0, bh[0], bl[0]);
+  split_tf32(b1, bh[1], bl[1]);
+  mma_tf32(d, al, bh[0], bh[1]);
+  mma_tf32(d, ah, bl[0], bl[1]);
+  mma_tf32(d, ah, bh[0], bh[1]);
+}
+__device__ __forceinline__ float lds32(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 lds128(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // An item as every lane of its warp sees it; `mine` is what row `lane` sees.
-struct WarpItem {
-  int b, j, part, nrows;
-  int64_t row0;       // first new token among all
-  int lo, hi;         // positions that the rows see together
-  int first, last;    // the steps of this run
+struct Item {
+  int j, part, nrows;      // KV head, partial result, rows
+  int64_t row0;            // first new token among all
+  const int32_t* table;
+  int lo, hi;              // positions that the rows see together
+  int first, last;         // the steps of this run
   pa::Span mine;
 };
-__device__ __forceinline__ WarpItem open_item(const Args& a, int w, bool tell) {
-  const int lane = threadIdx.x & 31;
-  WarpItem it;
-  it.part = w % a.own_parts;
-  const int rest = w / a.own_parts;
-  it.j = rest % a.Hkv, it.b = rest / a.Hkv;
-  const pa::Seq s = pa::seq_of(a, it.b, tell && lane == 0 && it.part == 0 && it.j == 0);
-  it.row0 = s.first;
-  it.nrows = (int)s.n_new * a.g;
+// Items are the runs of the shared prefix first (fp32: rows of all sequences
+// side by side), then those of the sequences' own tokens.
+template <typename T>
+__device__ __forceinline__ Item open_item(const Args& a, int w, bool tell) {
+  const int lane = threadIdx.x & 31, tpt = kRows / a.g;
+  Item it;
+  // in bf16 the prefix, and sequences of more than 16 rows, go to the
+  // tensor-core kernel
+  const bool prefix = sizeof(T) == 4 && w < a.prefix_items;
+  if (!prefix) w -= a.prefix_items;
+  const int parts = prefix ? a.prefix_parts : a.own_parts, run = w % parts, rest = w / parts;
+  it.j = rest % a.Hkv;
+  it.part = prefix ? run : a.prefix_parts + run;
+  const int at = rest / a.Hkv;
   it.mine = pa::Span{0, INT32_MAX, 0};  // padding rows see everything: no masks for their sake
   int lo = INT32_MAX, hi = 0;
-  if (lane < it.nrows) {
-    it.mine = pa::span_of(a, s, it.b, lane / a.g);
-    if (it.mine.lo < it.mine.hi) lo = it.mine.lo, hi = it.mine.hi;
+  if (prefix) {
+    it.row0 = (int64_t)at * tpt;
+    it.nrows = (int)min((int64_t)tpt, a.T - it.row0) * a.g;
+    it.table = a.prefix_table;
+    if (lane < it.nrows) {
+      const int64_t n = min((int64_t)max(a.n_tok[it.row0 + lane / a.g], 0), a.n_max);
+      it.mine = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
+    }
+  } else {
+    const int tiles = sizeof(T) == 4 ? (a.max_q + tpt - 1) / tpt : 1, b = at / tiles, i0 = at % tiles * tpt;
+    const pa::Seq s = pa::seq_of(a, b, tell && lane == 0 && run == 0 && it.j == 0 && i0 == 0);
+    it.row0 = s.first + i0;
+    it.nrows = (int)min((int64_t)tpt, max(s.n_new - i0, (int64_t)0)) * a.g;
+    it.table = a.pm.table + (int64_t)b * a.pm.max_pages;
+    if (lane < it.nrows) it.mine = pa::span_of(a, s, b, i0 + lane / a.g);
   }
+  if (lane < it.nrows && it.mine.lo < it.mine.hi) lo = it.mine.lo, hi = it.mine.hi;
   hi = __reduce_max_sync(0xffffffffu, hi);
   lo = min(__reduce_min_sync(0xffffffffu, lo), hi);
   it.lo = lo, it.hi = hi;
-  const int s0 = lo / kStep, s1 = (hi + kStep - 1) / kStep, per = (s1 - s0 + a.own_parts - 1) / a.own_parts;
-  it.first = s0 + it.part * per;
+  constexpr int S = kStep<T>;
+  const int s0 = lo / S, s1 = (hi + S - 1) / S, per = (s1 - s0 + parts - 1) / parts;
+  it.first = s0 + run * per;
   it.last = hi > lo ? min(s1, it.first + per) : it.first;
   return it;
 }
 
-template <bool kGeneral>
+template <typename T, bool kGeneral>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-rows_mma_kernel(const __grid_constant__ Args a, int items) {
-  constexpr int D = kHeadDim;
+rows_kernel(const __grid_constant__ Args a, int items) {
+  constexpr int D = kHeadDim, S = kStep<T>, NT = S / 8;  // tiles of 8 tokens in a step
+  constexpr bool kBf16 = sizeof(T) == 2;
+  constexpr uint32_t kAll = (1u << S) - 1;
   extern __shared__ __align__(1024) unsigned char ring[];  // [warp][stage][K step, V step]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3, r8 = lane >> 2;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the prefix's kernel may take the other SMs
   const int worker = warp * gridDim.x + blockIdx.x, workers = gridDim.x * kWarps;
   const uint32_t P = a.pm.page_size, pages = (uint32_t)a.pm.num_pages;
   const uint32_t my_ring = sm32(ring) + warp * kStages * 2 * kStepBytes;
 
   // ---- where the loads are: item, step, and the page of this lane's token ----
-  // A step's tokens are brought two whole rows at a time (64 bytes of eight rows
-  // at a time took longer); piece c of token x lies at c ^ (x % 8).
+  // A step's rows are brought whole, 512 bytes an instruction (64 bytes of
+  // eight rows at a time took longer).  Their 16-byte pieces are permuted by
+  // the row so that the fragments' reads meet no bank twice: in bf16 piece c of
+  // token x lies at c ^ (x % 8); in fp32 at c ^ 4 (x % 2) for K, whose readers
+  // take four pieces of eight tokens, and at c ^ 2 (x / 2) for V, whose readers
+  // take two pieces of every other token.
   int p_w = worker, p_step = 0, p_last = 0, p_lo = 0, p_hi = 0, p_j = 0, p_page = -1;
   const int32_t* __restrict__ p_table = nullptr;
   auto page_of = [&]() -> int {
-    const uint32_t u = (uint32_t)p_step * kStep + (lane & 15);
+    const uint32_t u = (uint32_t)p_step * S + (lane & (S - 1));
     return p_step < p_last && (int)u >= p_lo && (int)u < p_hi ? p_table[u / P] : -1;
   };
   auto open_loads = [&] {
-    const WarpItem it = open_item(a, p_w, true);
+    const Item it = open_item<T>(a, p_w, true);
     p_step = it.first, p_last = it.nrows > 0 ? it.last : it.first, p_lo = it.lo, p_hi = it.hi, p_j = it.j;
-    p_table = a.pm.table + (int64_t)it.b * a.pm.max_pages;
+    p_table = it.table;
     p_page = page_of();
   };
   // Bits 16 s ..: which tokens of the step loaded s steps ago have a place in
@@ -366,39 +192,43 @@ rows_mma_kernel(const __grid_constant__ Args a, int items) {
     }
     bool ok = false;
     if (p_w < items) {
-      const uint32_t u = (uint32_t)p_step * kStep + (lane & 15);
+      const uint32_t u = (uint32_t)p_step * S + (lane & (S - 1));
       const bool in = (int)u >= p_lo && (int)u < p_hi;
       ok = in && (uint32_t)p_page < pages;
-      if (in && !ok && lane < 16) report(a.status, HKV_ERR_DEVICE_RANGE);
+      if (in && !ok && lane < S) report(a.status, HKV_ERR_DEVICE_RANGE);
       const uint32_t row = ok ? ((uint32_t)p_page * a.Hkv + p_j) * P + u % P : 0xffffffffu;
       const uint32_t base = my_ring + slot * 2 * kStepBytes;
-      const int c = lane & 15;
+      constexpr int kPieces = kStepBytes / S / 16, kRowsAt = 32 / kPieces;  // 16-byte pieces of a row; rows an instruction
+      const int c = lane & (kPieces - 1);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int x = 2 * i + (lane >> 4);
+        const int x = kRowsAt * i + lane / kPieces;
         const uint32_t rx = __shfl_sync(0xffffffffu, row, x);
-        const uint32_t dst = base + x * 256 + ((c ^ (x & 7)) << 4);
-        const int64_t off = rx == 0xffffffffu ? 0 : (int64_t)rx * D + c * 8;
+        const uint32_t k_to = base + x * (kStepBytes / S) + ((kBf16 ? c ^ (x & 7) : c ^ ((x & 1) << 2)) << 4);
+        const uint32_t v_to = base + kStepBytes + x * (kStepBytes / S) + ((kBf16 ? c ^ (x & 7) : c ^ ((x >> 1) << 1)) << 4);
+        const int64_t off = rx == 0xffffffffu ? 0 : (int64_t)rx * D + c * (16 / (int)sizeof(T));
         const int bytes = rx == 0xffffffffu ? 0 : 16;
-        cp16(dst, static_cast<const __nv_bfloat16*>(a.K) + off, bytes);
-        cp16(dst + kStepBytes, static_cast<const __nv_bfloat16*>(a.V) + off, bytes);
+        cp16(k_to, static_cast<const T*>(a.K) + off, bytes);
+        cp16(v_to, static_cast<const T*>(a.V) + off, bytes);
       }
       ++p_step;
       p_page = page_of();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    there_of = there_of << 16 | (__ballot_sync(0xffffffffu, ok) & 0xffffu);
+    there_of = there_of << 16 | (__ballot_sync(0xffffffffu, ok) & kAll);
     if (++slot == kStages) slot = 0;
   };
-  // The first lines that an item needs, the start of its page table and its
-  // queries, are called into L2 while the warp's item before it is worked on.
+  // The first lines that an own item needs, the start of its page table and its
+  // queries, are called into L2 while the warp's items before it are worked on.
   auto call_in = [&](int w) {
-    if (w >= items) return;
-    const int rest = w / a.own_parts, j = rest % a.Hkv, b = rest / a.Hkv;
-    const int64_t tok = a.cu ? a.cu[b] : b;
+    if (w >= items || w < a.prefix_items) return;
+    const int rest = (w - a.prefix_items) / a.own_parts, j = rest % a.Hkv, tpt = kRows / a.g;
+    const int tiles = kBf16 ? 1 : (a.max_q + tpt - 1) / tpt, b = rest / a.Hkv / tiles;
+    const int64_t tok = (a.cu ? a.cu[b] : b) + rest / a.Hkv % tiles * tpt;
+    constexpr int kLine = 128 / (int)sizeof(T);
     const void* at = lane == 0 ? static_cast<const void*>(a.pm.table + (int64_t)b * a.pm.max_pages)
-                               : static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride + (int64_t)j * a.g * D + (lane - 1) * 64;
-    if (lane <= 2 * a.g && (lane == 0 || tok < a.T)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                               : static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)j * a.g * D + (lane - 1) * kLine;
+    if (lane == 0 || (lane <= a.g * D / kLine && tok >= 0 && tok < a.T)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
   };
   call_in(worker);
   call_in(worker + workers);
@@ -408,69 +238,82 @@ rows_mma_kernel(const __grid_constant__ Args a, int items) {
 
   const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
   const float cap = a.softcap * pa::kLog2e;
-  const int parts = a.prefix_parts + a.own_parts;
+  const bool whole_rows = a.prefix_parts + a.own_parts == 1;  // rows are finished here
 #pragma unroll 1
   for (int w = worker; w < items; w += workers) {
     call_in(w + 2 * workers);
-    const WarpItem it = open_item(a, w, false);
+    const Item it = open_item<T>(a, w, false);
     if (it.nrows == 0) continue;
-    // this thread's two rows of every fragment, and the queries of them: A
-    // fragments straight from memory
+    // this thread's two rows of every fragment, and their queries as A fragments
     pa::Span sp[2];
     float slope[2];
-    uint32_t qf[8][4];
+    uint32_t qf[kBf16 ? 8 : 1][4];    // bf16: k = kk * 16 ..
+    float4 qv[kBf16 ? 1 : 8][2];      // fp32: elements 16 kk + 4 c4 .. of both rows, two k steps of four
     int64_t row_at[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = lane / 4 + 8 * h;
+      const int r = r8 + 8 * h;
       sp[h] = pa::Span{__shfl_sync(0xffffffffu, it.mine.lo, r), __shfl_sync(0xffffffffu, it.mine.hi, r),
                        __shfl_sync(0xffffffffu, it.mine.pos, r)};
       const int head = it.j * a.g + r % a.g;
       slope[h] = kGeneral && a.slopes && r < it.nrows ? a.slopes[head] * pa::kLog2e : 0.f;
       row_at[h] = (it.row0 + r / a.g) * a.Hq + head;
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + r / a.g) * a.q_stride +
-                                                            (int64_t)head * D) + lane % 4;
+      const T* q = static_cast<const T*>(a.q) + (it.row0 + r / a.g) * a.q_stride + (int64_t)head * D;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        qf[kk][h] = r < it.nrows ? __ldg(q + kk * 8) : 0u;
-        qf[kk][2 + h] = r < it.nrows ? __ldg(q + kk * 8 + 4) : 0u;
+        if constexpr (kBf16) {
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(q) + kk * 8 + c4;
+          qf[kk][h] = r < it.nrows ? __ldg(p) : 0u;
+          qf[kk][2 + h] = r < it.nrows ? __ldg(p + 4) : 0u;
+        } else {
+          qv[kk][h] = r < it.nrows ? __ldg(reinterpret_cast<const float4*>(q) + kk * 4 + c4) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       }
     }
     float acc[16][4] = {};
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll 1
     for (int step = it.first; step < it.last; ++step) {
-      const uint32_t there = (uint32_t)(there_of >> (16 * (kStages - 2))) & 0xffffu;
+      const uint32_t there = (uint32_t)(there_of >> (16 * (kStages - 2))) & kAll;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();
       // `slot` is the next one to fill, which the last step left: this step's is one on
       const uint32_t kb = my_ring + (slot + 1 == kStages ? 0 : slot + 1) * 2 * kStepBytes, vb = kb + kStepBytes;
-      float z[2][4] = {}, y[2][4] = {};  // even and odd kk: half as long a chain of MMAs
+      float z[NT][4] = {}, y[NT][4] = {};  // even and odd kk: half as long a chain of MMAs
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        // tokens 0-7 and 8-15 of the step, elements kk * 16 + 0-7 and 8-15
-        uint32_t b[4];
-        const int x = (lane & 7) + (lane >> 4) * 8, ch = kk * 2 + ((lane >> 3) & 1);
-        ldsm4(b, kb + x * 256 + ((ch ^ (x & 7)) << 4));
-        mma16816(kk & 1 ? y[0] : z[0], qf[kk], b[0], b[1]);
-        mma16816(kk & 1 ? y[1] : z[1], qf[kk], b[2], b[3]);
+        if constexpr (kBf16) {
+          // tokens 0-7 and 8-15 of the step, elements kk * 16 + 0-7 and 8-15
+          uint32_t b[4];
+          const int x = (lane & 7) + (lane >> 4) * 8, ch = kk * 2 + ((lane >> 3) & 1);
+          ldsm4(b, kb + x * 256 + ((ch ^ (x & 7)) << 4));
+          mma16816(kk & 1 ? y[0] : z[0], qf[kk], b[0], b[1]);
+          mma16816(kk & 1 ? y[NT - 1] : z[NT - 1], qf[kk], b[2], b[3]);
+        } else {
+          // token r8, elements 16 kk + 4 c4 ..: the order of the sum's terms is free
+          const float4 b = lds128(kb + r8 * 512 + (((kk * 4 + c4) ^ ((r8 & 1) << 2)) << 4));
+          const float4 u = qv[kk][0], v = qv[kk][1];
+          const float a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+          mma_fp32(z[0], a0, b.x, b.y);
+          mma_fp32(y[0], a1, b.z, b.w);
+        }
       }
       load_next();  // here, where the scores are not there yet
-      const int u0 = step * kStep + (lane & 3) * 2;  // this thread's tokens: u0, u0 + 1, u0 + 8, u0 + 9
+      const int u0 = step * S + c4 * 2;  // this thread's tokens: u0, u0 + 1 (and u0 + 8, u0 + 9)
       float top[2] = {-INFINITY, -INFINITY};
-      const bool whole = there == 0xffffu && sp[0].lo <= step * kStep && sp[1].lo <= step * kStep &&
-                         sp[0].hi >= (step + 1) * kStep && sp[1].hi >= (step + 1) * kStep;
+      const bool whole = there == kAll && sp[0].lo <= step * S && sp[1].lo <= step * S && sp[0].hi >= (step + 1) * S &&
+                         sp[1].hi >= (step + 1) * S;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = e >> 1, u = u0 + n * 8 + (e & 1);
           float x = (z[n][e] + y[n][e]) * zs;
           if (kGeneral) {
-            if (cap > 0.f) x = pa::capped(x, cap);
+            if (cap > 0.f) x = kBf16 ? pa::capped(x, cap) : cap * tanhf(x);
             x = fmaf(-slope[h], fabsf((float)(sp[h].pos - u)), x);
           }
-          if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there >> (u & 15) & 1u))) x = -INFINITY;
+          if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there >> (u & (S - 1)) & 1u))) x = -INFINITY;
           z[n][e] = x;
           top[h] = fmaxf(top[h], x);
         }
@@ -491,22 +334,33 @@ rows_mma_kernel(const __grid_constant__ Args a, int items) {
         }
       }
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = e >> 1;
-          z[n][e] = pa::ex2(z[n][e] - (m[h] == -INFINITY ? 0.f : m[h]));
+          const float x = z[n][e] - (m[h] == -INFINITY ? 0.f : m[h]);
+          z[n][e] = kBf16 ? pa::ex2(x) : exp2f(x);
           l[h] += z[n][e];
         }
-      const uint32_t pf[4] = {pack2(z[0][0], z[0][1]), pack2(z[0][2], z[0][3]), pack2(z[1][0], z[1][1]),
-                              pack2(z[1][2], z[1][3])};
+      if constexpr (kBf16) {
+        const uint32_t pf[4] = {pack2(z[0][0], z[0][1]), pack2(z[0][2], z[0][3]), pack2(z[NT - 1][0], z[NT - 1][1]),
+                                pack2(z[NT - 1][2], z[NT - 1][3])};
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        uint32_t b[4];
-        const int x = lane & 15, ch = d * 2 + (lane >> 4);
-        ldsm4t(b, vb + x * 256 + ((ch ^ (x & 7)) << 4));
-        mma16816(acc[2 * d], pf, b[0], b[1]);
-        mma16816(acc[2 * d + 1], pf, b[2], b[3]);
+        for (int d = 0; d < 8; ++d) {
+          uint32_t b[4];
+          const int x = lane & 15, ch = d * 2 + (lane >> 4);
+          ldsm4t(b, vb + x * 256 + ((ch ^ (x & 7)) << 4));
+          mma16816(acc[2 * d], pf, b[0], b[1]);
+          mma16816(acc[2 * d + 1], pf, b[2], b[3]);
+        }
+      } else {
+        // k = c4 is token 2 c4 and k = c4 + 4 token 2 c4 + 1, as the weights lie
+        const float pf[4] = {z[0][0], z[0][2], z[0][1], z[0][3]};
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+          const uint32_t at = vb + c4 * 1024 + (((2 * d + (lane >> 4)) ^ (c4 << 1)) << 4) + (r8 & 3) * 4;
+          mma_fp32(acc[d], pf, lds32(at), lds32(at + 512));
+        }
       }
       __syncwarp();
     }
@@ -515,19 +369,22 @@ rows_mma_kernel(const __grid_constant__ Args a, int items) {
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-      if (lane / 4 + 8 * h >= it.nrows) continue;
-      if (parts > 1) {
-        const int64_t row = (a.prefix_parts + it.part) * a.T * a.Hq + row_at[h];
-        if ((lane & 3) == 0) a.part_ml[row] = make_float2(m[h], l[h]);
-        float2* dst = reinterpret_cast<float2*>(a.part_o + row * D) + (lane & 3);
+      if (r8 + 8 * h >= it.nrows) continue;
+      const bool any = l[h] > 0.f;
+      const float by = !whole_rows ? 1.f : any ? 1.f / l[h] : 0.f;
+      const int64_t row = row_at[h] + (whole_rows ? 0 : it.part * a.T * a.Hq);
+      if (c4 == 0) {
+        if (!whole_rows) a.part_ml[row] = make_float2(m[h], l[h]);
+        else if (a.lse) a.lse[row] = any ? (m[h] + log2f(l[h])) * pa::kLn2 : -INFINITY;
+      }
+      if (kBf16 && whole_rows) {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + c4;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dst[i * 4] = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+        for (int i = 0; i < 16; ++i) dst[i * 4] = pack2(acc[i][2 * h] * by, acc[i][2 * h + 1] * by);
       } else {
-        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
-        if ((lane & 3) == 0 && a.lse) a.lse[row_at[h]] = l[h] > 0.f ? (m[h] + log2f(l[h])) * pa::kLn2 : -INFINITY;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row_at[h] * D) + (lane & 3);
+        float2* dst = reinterpret_cast<float2*>((whole_rows ? static_cast<float*>(a.out) : a.part_o) + row * D) + c4;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dst[i * 4] = pack2(acc[i][2 * h] * inv, acc[i][2 * h + 1] * inv);
+        for (int i = 0; i < 16; ++i) dst[i * 4] = make_float2(acc[i][2 * h] * by, acc[i][2 * h + 1] * by);
       }
     }
   }
@@ -586,15 +443,15 @@ join_parts_kernel(const __grid_constant__ Args a) {
 }
 
 // Runs of positions that an item is cut into.  Few items are cut until every
-// worker has one, down to 128 tokens; many items only into runs of at least
-// 512 tokens, six for every worker, so that the last ones to run are short.
-int splits_for(int64_t items, int64_t tokens, int64_t workers) {
+// worker has one, down to eight steps; many items only into runs of at least
+// 32 steps, six for every worker, so that the last ones to run are short.
+int splits_for(int64_t items, int64_t tokens, int64_t workers, int step) {
   auto cut = [&](int64_t want, int64_t least) {
     want = ceil_div(want, items < 1 ? 1 : items);
     const int64_t most = ceil_div(tokens, least);
     return want < most ? want : most;
   };
-  const int64_t few = cut(workers, 128), many = cut(6 * workers, 512), s = few > many ? few : many;
+  const int64_t few = cut(workers, 8 * step), many = cut(6 * workers, 32 * step), s = few > many ? few : many;
   return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
@@ -604,7 +461,8 @@ struct Plan {
   bool tc = false;         // prompts: the tensor-core kernel takes all rows
   int64_t own_items = 0;   // rows of one sequence (16 at most), all KV heads together
   int prefix_parts = 0, own_parts = 1;
-  int row_ctas = 0;        // bf16: blocks of the single-token kernel, one per SM
+  int prefix_items = 0;    // fp32: runs of the prefix that the same kernel takes
+  int row_ctas = 0;        // blocks of this file's kernel, one per SM
   int parts = 0;           // a row's partial results, 0 when its block finishes it
   size_t o = 0, total = 0;  // byte offset of part_o behind part_ml, and the size
 };
@@ -619,9 +477,14 @@ Plan plan(const PagedAttend& p) {
     r.own_parts = tc_splits(p, false, sms);
   } else {
     r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt) * p.Hkv;
-    // two fp32 blocks, or eight bf16 warps, per SM
-    r.own_parts = splits_for(r.own_items, p.n_max, (bf16 ? kWarps : 2) * sms);
-    const int64_t items = r.own_items * r.own_parts;
+    r.own_parts = splits_for(r.own_items, p.n_max, kWarps * sms, bf16 ? kStep<__nv_bfloat16> : kStep<float>);
+    int64_t items = r.own_items * r.own_parts;
+    if (p.n_prefix > 0 && !bf16) {
+      const int64_t tiles = ceil_div(p.B, tpt) * p.Hkv;
+      r.prefix_parts = splits_for(tiles, p.n_prefix, kWarps * sms, kStep<float>);
+      r.prefix_items = (int)(tiles * r.prefix_parts);
+      items += r.prefix_items;
+    }
     r.row_ctas = (int)(items < sms ? items : sms);
     if (p.n_prefix > 0 && bf16) {
       // The prefix (bound by the tensor cores) and the sequences' own tokens
@@ -637,8 +500,6 @@ Plan plan(const PagedAttend& p) {
       r.row_ctas = share < 1 ? 1 : share > sms - sms / 8 ? sms - sms / 8 : share;
       if (r.row_ctas > items) r.row_ctas = (int)items;
       r.prefix_parts = tc_splits(p, true, sms - r.row_ctas);
-    } else if (p.n_prefix > 0) {
-      r.prefix_parts = splits_for(ceil_div(p.B, tpt) * p.Hkv, p.n_prefix, 2 * sms);
     }
   }
   r.parts = r.prefix_parts > 0 || r.own_parts > 1 ? r.prefix_parts + r.own_parts : 0;
@@ -647,37 +508,22 @@ Plan plan(const PagedAttend& p) {
   return r;
 }
 
-int run_fp32(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
-  constexpr size_t smem = kSimtStages * sizeof(SimtStage);
-  for (int prefix = pl.prefix_parts > 0; prefix >= 0; --prefix) {
-    auto kernel = prefix ? rows_simt_kernel<true> : rows_simt_kernel<false>;
-    const int rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem),
-                              "paged attention smem attribute");
-    if (rc != HKV_OK) return rc;
-    const int64_t blocks = prefix ? ceil_div(p.B, kRows / a.g) : pl.own_items / p.Hkv;
-    kernel<<<dim3((unsigned)blocks, p.Hkv, prefix ? pl.prefix_parts : pl.own_parts), kThreads, smem, st>>>(a);
-    const int rc2 = cuda_check(cudaGetLastError(), "paged attention launch");
-    if (rc2 != HKV_OK) return rc2;
-  }
-  return HKV_OK;
-}
-
-int run_bf16(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
-  if (pl.tc) return launch_attend_tc(p, a, false, pl.own_parts, pl.parts ? 0 : -1, st);
-  const int64_t items = pl.own_items * pl.own_parts;
-  if (items > INT32_MAX / 2) return fail(HKV_ERR_UNSUPPORTED, "too many sequences and heads");
-  auto kernel = a.softcap > 0.f || a.slopes ? rows_mma_kernel<true> : rows_mma_kernel<false>;
-  int rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes),
-                      "paged attention smem attribute");
-  if (rc != HKV_OK) return rc;
-  kernel<<<pl.row_ctas, kWarps * 32, kRingBytes, st>>>(a, (int)items);
-  rc = cuda_check(cudaGetLastError(), "paged attention launch");
-  return rc == HKV_OK && pl.prefix_parts > 0 ? launch_attend_tc(p, a, true, pl.prefix_parts, 0, st) : rc;
-}
-
 template <typename T>
 int run(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
-  const int rc = sizeof(T) == 2 ? run_bf16(p, pl, a, st) : run_fp32(p, pl, a, st);
+  int rc = HKV_OK;
+  if (pl.tc) {
+    rc = launch_attend_tc(p, a, false, pl.own_parts, pl.parts ? 0 : -1, st);
+  } else {
+    const int64_t items = pl.prefix_items + pl.own_items * pl.own_parts;
+    if (items > INT32_MAX / 2) return fail(HKV_ERR_UNSUPPORTED, "too many sequences and heads");
+    auto kernel = a.softcap > 0.f || a.slopes ? rows_kernel<T, true> : rows_kernel<T, false>;
+    rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes),
+                    "paged attention smem attribute");
+    if (rc != HKV_OK) return rc;
+    kernel<<<pl.row_ctas, kWarps * 32, kRingBytes, st>>>(a, (int)items);
+    rc = cuda_check(cudaGetLastError(), "paged attention launch");
+    if (rc == HKV_OK && sizeof(T) == 2 && pl.prefix_parts > 0) rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
+  }
   if (rc != HKV_OK || pl.parts == 0) return rc;
   return cuda_check(launch_after(join_parts_kernel<T>, dim3((unsigned)ceil_div(a.T * a.Hq, 4)), 128, 0, st, a),
                     "attention join launch");
@@ -699,7 +545,7 @@ int launch_attend_paged(const PagedAttend& p, void* ws, size_t ws_bytes, cudaStr
   a.scale = p.scale, a.softcap = p.softcap, a.window = p.window, a.slopes = p.slopes;
   a.prefix_len = p.prefix_len, a.q_first = p.q_first, a.out = p.out, a.lse = p.lse, a.status = p.status;
   a.wait_ns = wait_limit_ns();
-  a.prefix_parts = pl.prefix_parts, a.own_parts = pl.own_parts;
+  a.prefix_parts = pl.prefix_parts, a.own_parts = pl.own_parts, a.prefix_items = pl.prefix_items;
   unsigned char* w = static_cast<unsigned char*>(ws);
   a.part_ml = reinterpret_cast<float2*>(w);
   a.part_o = reinterpret_cast<float*>(w + pl.o);
