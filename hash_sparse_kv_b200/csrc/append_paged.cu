@@ -159,15 +159,14 @@ __device__ __forceinline__ float element(const Raw<float>& r, int k) {
   return __uint_as_float(p[k]);
 }
 
-// Products and sums rounded one by one, two at a time.
+// Products and sums rounded one by one (as packed f32x2 operations the products
+// came out fused with the sums).
 __device__ __forceinline__ void turn(uint64_t& lo, uint64_t& hi, uint64_t c, uint64_t s) {
-  uint64_t a, b, d, e;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(a) : "l"(lo), "l"(c));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(b) : "l"(hi), "l"(s));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(hi), "l"(c));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(e) : "l"(lo), "l"(s));
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(lo) : "l"(a), "l"(b));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(hi) : "l"(d), "l"(e));
+  const float2 a = unpair(lo), b = unpair(hi), co = unpair(c), si = unpair(s);
+  const float x = __fsub_rn(__fmul_rn(a.x, co.x), __fmul_rn(b.x, si.x)), y = __fsub_rn(__fmul_rn(a.y, co.y), __fmul_rn(b.y, si.y));
+  const float z = __fadd_rn(__fmul_rn(b.x, co.x), __fmul_rn(a.x, si.x)), w = __fadd_rn(__fmul_rn(b.y, co.y), __fmul_rn(a.y, si.y));
+  lo = pair(__float_as_uint(x), __float_as_uint(y));
+  hi = pair(__float_as_uint(z), __float_as_uint(w));
 }
 
 // Sine and cosine in fp64 of any angle below 2^31 turns: the nearest multiple n

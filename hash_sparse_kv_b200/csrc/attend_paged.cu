@@ -16,9 +16,9 @@
 // 128-row tcgen05 tile would be seven eighths padding, so scores and products
 // are mma.sync with the 16 rows as M.
 //   bf16: m16n8k16; P is rounded to bf16 for the product, sums stay fp32.
-//   fp32: m16n8k8 tf32 in three products.  x = hi + lo with hi the upper 19
-//         bits of x; hi hi + hi lo + lo hi leaves out lo lo and what tf32 drops
-//         of lo, 2^-21 of a product, beside fp32's own 2^-24 for each of 128.
+//   fp32: m16n8k8 tf32 in three products.  x = hi + lo, both rounded to tf32's
+//         11 bits; hi hi + hi lo + lo hi leaves out lo lo and the rounding of
+//         lo, each 2^-24 of a product at most, as much as fp32's own rounding.
 #include <cstdio>
 
 #include "attend_paged.cuh"
@@ -67,9 +67,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Both parts rounded to the nearest tf32 (half a step is added, and the bits
+// below are dropped here or by the instruction): dropping bits of hi alone
+// would leave errors of one sign.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 // d += a b for fp32 a (16 x 8) and b (8 x 8).
 __device__ __forceinline__ void mma_fp32(float (&d)[4], const float (&a)[4], float b0, float b1) {
