@@ -74,10 +74,10 @@ def spans(n, n_new, window=0, prefix=0, first=None):
 
 def score_error(q, K, scale):
     """Largest error of a score: the products of bf16 or fp32 values summed in fp32, 128 of them, in any order, and the
-    few operations behind: (128 + 8) roundings of 2^-24 on at most scale * |q| |k|."""
+    few operations behind: (128 + 8) roundings of 2^-24 on at most |scale| |q| |k|."""
     if K.numel() == 0:
         return 0.0
-    return 136 * 2.0 ** -24 * scale * float(q.double().norm(dim=-1).max() * torch.nan_to_num(K.double()).norm(dim=-1).max())
+    return 136 * 2.0 ** -24 * abs(scale) * float(q.double().norm(dim=-1).max() * torch.nan_to_num(K.double()).norm(dim=-1).max())
 
 
 def check(out, lse, want, dtype, dz, n):

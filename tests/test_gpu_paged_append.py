@@ -202,3 +202,44 @@ def test_captured_and_replayed():
     V = a["V_pool"].cpu()
     got = [V[0, 0, 2], V[0, 0, 3], V[3, 0, 2], V[3, 0, 3]]  # positions 2, 3 and 6, 7
     assert torch.equal(torch.stack(got), a["v_new"][:, 0].cpu()) and int((V != 0).any(-1).sum()) == 4
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_products_and_sums_are_rounded_one_by_one(dt, inter):
+    """Angles in 64 bits, sine and cosine rounded to 32, then separate fp32 products and sums: the same bits.  The two
+    sides' 64-bit sines differ by less than 2^-44, so one in 2^19 may round apart: none of 4096 values may."""
+    g = torch.Generator().manual_seed(31)
+    T, H, pairs = 64, 3, 64
+    x, pos = torch.randn(T, H, D, generator=g).to(dt), torch.randint(0, 100000, (1, T), generator=g, dtype=torch.int32)
+    K = torch.zeros(1, H, T, D, dtype=dt, device=DEV)
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    hkv.hkv_append_paged(None, x.to(DEV), x.to(DEV), K, K.clone(), i([[0]]), i([0, T]), i([0]),
+                         rope=hkv.RopeParams(_inv(pairs).to(DEV), interleaved=inter), positions=pos.to(DEV))
+    a = pos[0].double()[:, None] * _inv(pairs).double()
+    c, s = a.cos().float()[:, None], a.sin().float()[:, None]
+    xf = x.float()
+    lo, hi = (xf[..., 0::2], xf[..., 1::2]) if inter else (xf[..., :pairs], xf[..., pairs:])
+    u, w = lo * c - hi * s, hi * c + lo * s
+    want = (torch.stack([u, w], -1).flatten(-2) if inter else torch.cat([u, w], -1)).to(dt)
+    assert torch.equal(K[0].cpu().transpose(0, 1), want)
+
+
+def test_two_calls_at_once():
+    """Two appends to different pages of one pool on two streams."""
+    a, b = _small(), _small()
+    for k in ("K_pool", "V_pool"):
+        b[k] = a[k]
+    a["page_table"], a["cu_new"], a["n_past"] = a["page_table"][:1], a["cu_new"][:2] * 2, a["n_past"][:1]
+    b["page_table"], b["cu_new"], b["n_past"] = b["page_table"][1:] + 2, b["cu_new"][:2] * 2, b["n_past"][1:] * 0
+    for x in (a, b):
+        for k in ("k_new", "v_new"):
+            x[k] = torch.randn_like(x[k])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s, x in zip(streams, (a, b)):
+        s.wait_stream(torch.cuda.current_stream())
+        hkv.hkv_append_paged(None, stream=s, **x)
+    torch.cuda.synchronize()
+    V = a["V_pool"].cpu()
+    assert torch.equal(torch.cat([V[0, 0, 1:], V[1, 0, :1]]), a["v_new"][:, 0].cpu())
+    assert torch.equal(V[4, 0], b["v_new"][:, 0].cpu())

@@ -87,6 +87,11 @@ PROMPTS = [
     (BF, 32, 8, 64, [40], [9000], {}),       # few rows over many pages: split
     (BF, 4, 2, 16, [120], [120], dict(scale=0.0)),
     (BF, 4, 2, 16, [120], [400], dict(scale=1.0, spread=1.0)),   # scores of tens: one key takes nearly all
+    (BF, 4, 4, 8, [20, 0, 3, 33] * 20, [20, 7, 90, 200] * 20, {}),   # 80 sequences
+    (BF, 4, 2, 1000, [300, 5], [2900, 1001], dict(window=700)),
+    (BF, 5, 1, 3, [60], [3000], dict(softcap=50.0, spread=30.0)),     # no TMA box, split, scores past the cap
+    (BF, 8, 2, 40, [31, 64], [31, 64], dict(softcap=30.0, scale=-0.1)),
+    (BF, 8, 2, 40, [31, 64], [31, 64], dict(scale=-0.05)),
     (F32, 8, 2, 5, [37, 1, 0, 12], [300, 1, 4, 12], {}),
     (F32, 4, 4, 64, [70], [500], dict(softcap=10.0, window=100, slopes=True, spread=3.0)),
     (F32, 16, 1, 16, [9, 20], [9, 90], dict(prefix=[6, 80], docs=11)),
@@ -242,6 +247,92 @@ def test_masked_keys_may_hold_anything(new):
     pos, lo, hi = spans(n, new, first=torch.full((new,), first))
     want = attend(q.cpu(), flat.nan_to_num(0.0, 0.0, 0.0), toks[0], pos, lo, hi, 1 / math.sqrt(D))
     check(out.cpu(), lse.cpu(), want, BF, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), n)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [1, 60])
+def test_pages_behind_the_window_may_be_gone(new, dt):
+    """A cache that gives back the pages its window has left: their table entries name no page."""
+    n, P, Hq, window = 700, 16, 4, 100
+    toks, pool, table = _cache(1, n, dt=dt)
+    table[0, :(n - new + 1 - window) // P] = -1
+    q = torch.randn(new, Hq, D, device=DEV).to(dt)
+    out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q, pool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, window=window, status=st,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt))
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    pos, lo, hi = spans(n, new, window)
+    K = toks[0].nan_to_num(0.0)
+    want = attend(q.cpu(), K, K, pos, lo, hi, 1 / math.sqrt(D))
+    check(out.cpu(), lse.cpu(), want, dt, score_error(q.cpu(), K, 1 / math.sqrt(D)), n)
+
+
+def test_sequences_may_share_pages_and_calls_may_overlap():
+    """The same pages in two sequences' tables, and two calls on two streams with a workspace each."""
+    n, Hq, new = 900, 8, 40
+    toks, pool, table = _cache(1, n)
+    table = table.repeat(2, 1)
+    calls = []
+    for k in range(2):
+        q = torch.randn(2 * new, Hq, D, device=DEV).to(BF)
+        out, lse = torch.zeros(2 * new, Hq, D, dtype=BF, device=DEV), torch.zeros(2 * new, Hq, device=DEV)
+        ws = hkv.prefill_workspace(2, Hq, 2, 2 * new, new, n)
+        calls.append((q, out, lse, ws))
+    cu, total, streams = _i([0, new, 2 * new]), _i([n, 500]), [torch.cuda.Stream() for _ in range(2)]
+    for s, (q, out, lse, ws) in zip(streams, calls):
+        s.wait_stream(torch.cuda.current_stream())
+        hkv.hkv_prefill_attend_paged(q, pool, pool, table, cu, total, new, n, out, lse=lse, ws=ws, stream=s)
+    torch.cuda.synchronize()
+    for q, out, lse, _ in calls:
+        for b, m in enumerate((n, 500)):
+            pos, lo, hi = spans(m, new)
+            at = slice(b * new, (b + 1) * new)
+            want = attend(q[at].cpu(), toks[0][:m], toks[0][:m], pos, lo, hi, 1 / math.sqrt(D))
+            check(out[at].cpu(), lse[at].cpu(), want, BF, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), m)
+
+
+def test_a_serving_step_in_one_graph():
+    """Append, shared-prefix decode and dense decode captured together and replayed on new inputs equal the eager calls
+    bit for bit."""
+    B, Hq, Hkv, P, n_prefix, past = 5, 8, 2, 16, 200, 37
+    g = torch.Generator().manual_seed(12)
+    pages = -(-(past + 1) // P)
+    n = -(-n_prefix // P) + B * pages
+    K, V = (torch.randn(n, Hkv, P, D, generator=g).to(BF).to(DEV) for _ in range(2))
+    order = torch.randperm(n, generator=g).int().to(DEV)
+    prefix, table = order[:-(-n_prefix // P)].contiguous(), order[-(-n_prefix // P):].view(B, pages).contiguous()
+    rope = hkv.RopeParams((1e4 ** (-torch.arange(64, dtype=torch.float64) / 64)).float().to(DEV))
+    x = torch.randn(B, Hq + 2 * Hkv, D, generator=g).to(BF).to(DEV)
+    q = torch.empty(B, Hq, D, dtype=BF, device=DEV)
+    cu, before, own = _i(list(range(B + 1))), _i([past] * B), _i([past + 1] * B)
+    pos = torch.full((1, B), n_prefix + past, dtype=torch.int32, device=DEV)
+    res = [torch.empty(B, Hq, D, dtype=BF, device=DEV) for _ in range(2)] + [torch.empty(B, Hq, device=DEV) for _ in range(2)]
+    ws = [hkv.shared_workspace(B, Hq, Hkv, n_prefix, past + 1), hkv.prefill_workspace(B, Hq, Hkv, B, 1, past + 1)]
+
+    def step():
+        hkv.hkv_append_paged(None, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], K, V, table, cu, before, rope=rope, positions=pos,
+                             q=x[:, :Hq], q_out=q)
+        hkv.hkv_shared_attend_paged(q, K, V, prefix, n_prefix, table, own, past + 1, res[0], lse=res[2], ws=ws[0])
+        hkv.hkv_prefill_attend_paged(q, K, V, table, cu, own, 1, past + 1, res[1], lse=res[3], ws=ws[1])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    x.copy_(torch.randn_like(x))
+    for r in res:
+        r.zero_()
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [r.clone() for r in res]
+    step()
+    assert all(torch.equal(a, b) for a, b in zip(got, res))
+    assert not torch.equal(res[0], res[1])
 
 
 @pytest.mark.parametrize("new", [1, 64])
