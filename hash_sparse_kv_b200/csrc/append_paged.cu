@@ -32,10 +32,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRowLanes = 8;                     // lanes of one row
 constexpr int kKeyPitch = kHeadDim + 8;          // shared key rows: 272 bytes, conflict-free for ldmatrix
 constexpr int kMaxKeys = 64;                     // keys of a step in shared memory, unless one token has more
-// The projection's fragments leave room for two blocks per SM, with rows
-// further ahead; the others hide the memory's latency better with more warps.
-constexpr int blocks_per_sm(int hash) { return hash == 2 ? 3 : 4; }
+// Blocks per SM.  More warps hide the memory's latency best (16K prompt tokens
+// with the sign hash: 84, 76 and 72 us with two, three and four); the
+// projection's blocks, 70 KB each, fit three times, so their warps have two
+// groups of rows on their way instead of one.
 enum { kHashNone = 0, kHashSign = 1, kHashLsh = 2, kHashStage = 3 };
+constexpr int blocks_per_sm(int hash) { return hash == kHashLsh ? 3 : 4; }
 
 struct AppendArgs {
   int B, Hq, Hkv, parts, pairs, interleaved, words;  // parts: warps of one token
@@ -261,7 +263,7 @@ __device__ __forceinline__ uint16_t row_norm(const Raw<T>& a, const Raw<T>& b) {
 template <typename T, int HASH>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(HASH))
 append_paged_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int D = kHeadDim, kAhead = blocks_per_sm(HASH) == 2 ? 2 : 1;  // groups of four rows that a warp has on their way
+  constexpr int D = kHeadDim, kAhead = HASH == kHashLsh ? 2 : 1;  // groups of four rows that a warp has on their way
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(16) float cos_s[kWarps][64], sin_s[kWarps][64];  // of a warp's token
   __shared__ int64_t row_s[2][kWarps];               // kHashLsh: pool rows of a step's tokens
