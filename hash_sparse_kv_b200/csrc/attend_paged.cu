@@ -544,7 +544,6 @@ int launch_attend_paged(const PagedAttend& p, void* ws, size_t ws_bytes, cudaStr
   a.B = p.B, a.Hq = p.Hq, a.Hkv = p.Hkv, a.g = p.Hq / p.Hkv, a.T = p.T, a.max_q = p.max_q;
   a.q = p.q, a.q_stride = p.q_stride, a.K = p.K_pool, a.V = p.V_pool, a.pm = p.pm, a.cu = p.cu_q, a.n_tok = p.n_tok;
   a.n_max = p.n_max, a.prefix_table = p.prefix_table, a.n_prefix = p.n_prefix;
-  a.prefix_pages = p.n_prefix > 0 ? ceil_div(p.n_prefix, p.pm.page_size) : 0;
   a.scale = p.scale, a.softcap = p.softcap, a.window = p.window, a.slopes = p.slopes;
   a.prefix_len = p.prefix_len, a.q_first = p.q_first, a.out = p.out, a.lse = p.lse, a.status = p.status;
   a.wait_ns = wait_limit_ns();

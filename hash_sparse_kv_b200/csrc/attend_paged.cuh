@@ -33,7 +33,6 @@ struct Args {
   int64_t n_max;
   const int32_t* prefix_table;  // pages of the shared prefix, null without one
   int64_t n_prefix;             // tokens of the shared prefix
-  int64_t prefix_pages;
   float scale, softcap;
   int window;
   const float* slopes;
@@ -70,13 +69,12 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b, bool tell) {
 struct Span {
   int lo, hi, pos;
 };
-// Positions seen by new token i of sequence b (prefill: the own pages hold the
-// whole sequence).
+// Positions seen by new token i of sequence b, whose pages hold all of it.
 // `docs`: whether q_first counts.
 __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i, bool docs = true) {
   Span r;
-  // a call may hold more new tokens than the clamped length: positions below
-  // zero see nothing but a prefix
+  // more new tokens than the sequence has: positions below zero see nothing but
+  // a prefix
   const int64_t p = s.n - s.n_new + i;
   int64_t lo = 0, hi = p + 1;
   if (a.window > 0 && p + 1 - a.window > lo) lo = p + 1 - a.window;

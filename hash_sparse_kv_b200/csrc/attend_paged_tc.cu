@@ -142,20 +142,21 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// 2^x for two x in [-126, 8] without the special-function unit, whose 16
+// 2^x for two x in [-127, 8] without the special-function unit, whose 16
 // results a cycle are what a softmax of this shape waits for (128 x 128
 // exponentials take it as long as the tensor cores need for the tile's
 // products).  x = n + f, n the nearest integer (read off the low bits of
-// x + 1.5 * 2^23), 2^f by the degree-4 minimax polynomial on [-1/2, 1/2]
-// (relative error 2.7e-6), n added to the exponent.
+// x + 1.5 * 2^23), 2^f by the degree-4 minimax polynomial on [-1/2, 1/2] with
+// constant term 1 (relative error 2.9e-6), n added to the exponent.  At x = -127
+// that leaves exactly zero, so scores clamped there count for nothing.
 __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
   const float kMagic = 12582912.f;
   const uint64_t r = add2(x, pair(kMagic, kMagic));
   const uint64_t f = fma2(add2(r, pair(-kMagic, -kMagic)), pair(-1.f, -1.f), x);
-  uint64_t p = fma2(pair(9.570102207e-03f, 9.570102207e-03f), f, pair(5.591786280e-02f, 5.591786280e-02f));
-  p = fma2(p, f, pair(2.402474433e-01f, 2.402474433e-01f));
-  p = fma2(p, f, pair(6.931217909e-01f, 6.931217909e-01f));
-  p = fma2(p, f, pair(9.999992847e-01f, 9.999992847e-01f));
+  uint64_t p = fma2(pair(9.582852945e-03f, 9.582852945e-03f), f, pair(5.590642616e-02f, 5.590642616e-02f));
+  p = fma2(p, f, pair(2.402409911e-01f, 2.402409911e-01f));
+  p = fma2(p, f, pair(6.931241751e-01f, 6.931241751e-01f));
+  p = fma2(p, f, pair(1.f, 1.f));
   const float2 n = unpair(r), v = unpair(p);
   return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(n.x) << 23)),
                      __int_as_float(__float_as_int(v.y) + (__float_as_int(n.y) << 23)));
@@ -711,8 +712,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         for (int i = 0; i < 16; ++i) {
           uint64_t z = pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
           float2 x = unpair(fma2(z, decltype(raw)::value ? poly.factor(z) : c2, off2));
-          if (kPolyMask >> (i % 8) & 1)  // a masked score comes out as 2^-126
-            x = exp2_poly(pair(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)));
+          if (kPolyMask >> (i % 8) & 1)
+            x = exp2_poly(pair(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f)));
           else
             x = make_float2(pa::ex2(x.x), pa::ex2(x.y));
           sum[i & 1] = add2(sum[i & 1], pair(x.x, x.y));
@@ -790,7 +791,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         l = l * scale0 + l1 * scale1, m = top;
       }
       const bool partial = t.part0 >= 0;
-      const bool none = m == -INFINITY;  // nothing seen: O was never written, or means nothing
+      const bool none = m == -INFINITY;  // nothing seen: O was never written, or is zero
       const float inv = partial ? 1.f : none ? 0.f : 1.f / l;
       const int64_t out_row = (partial ? (t.part0 + split) * a.T * a.Hq : 0) + my_out;
       if (live && partial) a.part_ml[out_row] = make_float2(m, none ? 0.f : l);

@@ -249,6 +249,38 @@ def test_masked_keys_may_hold_anything(new):
     check(out.cpu(), lse.cpu(), want, BF, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), n)
 
 
+@pytest.mark.parametrize("slopes", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [1, 60])
+def test_a_masked_value_weighs_exactly_nothing(new, dt, slopes):
+    """Values near the type's largest in positions that no row sees, among seen ones of the same tiles: behind the window
+    and before the document's start.  Any weight but zero would show."""
+    n, P, Hq = 330, 16, 4
+    toks, kpool, table = _cache(1, n, dt=dt)
+    first = torch.full((new,), n - new - 27)
+    V = toks[0].clone()
+    V[:first[0]] = 3e38 * torch.sign(V[:first[0]].float())
+    vpool = kpool.clone()
+    for i, page in enumerate(table[0, :-(-n // P)].long().cpu()):
+        rows = V[i * P:(i + 1) * P]
+        vpool[page, :, :len(rows)] = rows.transpose(0, 1).to(DEV)
+    q = torch.randn(new, Hq, D, generator=torch.Generator().manual_seed(5)).to(dt)
+    sl = 2.0 ** -torch.arange(3, 7).float() if slopes else None
+    for window, q_first in ((28, None), (0, first)):
+        out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+        hkv.hkv_prefill_attend_paged(q.to(DEV), kpool, vpool, table, _i([0, new]), _i([n]), new, n, out, lse=lse,
+                                     window=window, slopes=None if sl is None else sl.to(DEV),
+                                     q_first=None if q_first is None else q_first.int().to(DEV), status=st,
+                                     ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt))
+        assert hkv.hkv_check(st) == hkv.HKV_OK
+        pos, lo, hi = spans(n, new, window, 0, q_first)
+        seen = V.clone()
+        seen[:first[0]] = 0
+        dz = score_error(q, toks[0], 1 / math.sqrt(D)) + (2.0 ** -23 * 0.125 * n if slopes else 0.0)
+        want = attend(q, toks[0], seen, pos, lo, hi, 1 / math.sqrt(D), slopes=sl)
+        check(out.cpu(), lse.cpu(), want, dt, dz, n)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("new", [1, 60])
 def test_pages_behind_the_window_may_be_gone(new, dt):
