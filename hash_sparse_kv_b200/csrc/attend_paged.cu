@@ -36,6 +36,12 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
+// NaN if either is: a row that sees a NaN is NaN as a whole.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -318,19 +324,19 @@ rows_kernel(const __grid_constant__ Args a, int items) {
           }
           if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there >> (u & (S - 1)) & 1u))) x = -INFINITY;
           z[n][e] = x;
-          top[h] = fmaxf(top[h], x);
+          top[h] = max_nan(top[h], x);
         }
       bool grown = false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
-        grown |= top[h] > m[h] + 8.f || (m[h] == -INFINITY && top[h] > -INFINITY);
+        top[h] = max_nan(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = max_nan(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        grown |= !(top[h] <= m[h] + 8.f);  // from nothing to something, and to NaN, too
       }
       if (__any_sync(0xffffffffu, grown)) {  // rare after the first steps
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float mn = fmaxf(m[h], top[h]), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
+          const float mn = max_nan(m[h], top[h]), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn);
           m[h] = mn, l[h] *= f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[i][2 * h] *= f, acc[i][2 * h + 1] *= f;
@@ -373,7 +379,7 @@ rows_kernel(const __grid_constant__ Args a, int items) {
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (r8 + 8 * h >= it.nrows) continue;
-      const bool any = l[h] > 0.f;
+      const bool any = l[h] != 0.f;  // NaN is something
       const float by = !whole_rows ? 1.f : any ? 1.f / l[h] : 0.f;
       const int64_t row = row_at[h] + (whole_rows ? 0 : it.part * a.T * a.Hq);
       if (c4 == 0) {
@@ -403,13 +409,15 @@ join_parts_kernel(const __grid_constant__ Args a) {
   constexpr int Q = kHeadDim / 4, kAhead = 4;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n_rows = a.T * a.Hq;
   const int lane = threadIdx.x & 31, parts = a.prefix_parts + a.own_parts;
-  if (row >= n_rows) return;
-  if (a.cu) {
+  bool mine = row < n_rows;
+  if (mine && a.cu) {
     const int64_t t = row / a.Hq;
     const pa::Seq s = pa::seq_of(a, pa::find_seq(a.cu, a.B, t), false);
-    if (t < s.first || t >= s.first + s.n_new) return;  // behind the last sequence
+    mine = t >= s.first && t < s.first + s.n_new;  // not behind the last sequence
   }
+  // by every block: a call must not be over before the kernel whose parts these are
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!mine) return;
   const float2* ml = a.part_ml + row;
   const float4* part = reinterpret_cast<const float4*>(a.part_o) + row * Q + lane;
   float M = -INFINITY;
@@ -421,9 +429,9 @@ join_parts_kernel(const __grid_constant__ Args a) {
   for (int p0 = 0; p0 < parts; p0 += 32) {
     // lane p holds the weight of part p0 + p; an empty part's values need not
     // have been written
-    const float2 mine = p0 + lane < parts ? ml[(p0 + lane) * n_rows] : make_float2(-INFINITY, 0.f);
-    const float w = mine.x == -INFINITY ? 0.f : exp2f(mine.x - M);
-    L = fmaf(w, mine.y, L);
+    const float2 one = p0 + lane < parts ? ml[(p0 + lane) * n_rows] : make_float2(-INFINITY, 0.f);
+    const float w = one.x == -INFINITY ? 0.f : exp2f(one.x - M);
+    L = fmaf(w, one.y, L);
     const int n = min(32, parts - p0);
     for (int p = 0; p < n; p += kAhead) {
       float4 x[kAhead];
@@ -440,9 +448,9 @@ join_parts_kernel(const __grid_constant__ Args a) {
   }
 #pragma unroll
   for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L != 0.f ? 1.f / L : 0.f;
   put4(static_cast<T*>(a.out) + row * kHeadDim + lane * 4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (lane == 0 && a.lse) a.lse[row] = L > 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[row] = L != 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
 }
 
 // Runs of positions that an item is cut into.  Few items are cut until every

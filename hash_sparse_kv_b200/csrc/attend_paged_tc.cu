@@ -132,14 +132,15 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// NaN if any is: a row that sees a NaN is NaN as a whole.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ float min3(float a, float b, float c) {
   float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // 2^x for two x in [-127, 8] without the special-function unit, whose 16
@@ -662,7 +663,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
               if (kMode == kCapped) mn[q] = min3(mn[q], __uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]));
             }
         }
-        top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), low = fminf(min3(mn[0], mn[1], mn[2]), mn[3]);
+        top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]), low = min3(min3(mn[0], mn[1], mn[2]), mn[3], mn[3]);
       };
       extremes();
       if constexpr (kMode == kCapped) {
@@ -677,7 +678,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
       }
       top *= c;  // c is positive: the largest value is the largest score
-      const bool grown = top > m + kGrowth || (m == -INFINITY && top > -INFINITY);
+      const bool grown = !(top <= m + kGrowth);  // from nothing to something, and to NaN, too
       if (__any_sync(0xffffffffu, grown)) {
         float f = 1.f;
         if (grown) f = pa::ex2(m - top), l *= f, m = top;  // m = -inf: 0
@@ -785,7 +786,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       float scale0 = 1.f;
       if (!both) {
         const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
-        const float top = fmaxf(m, m1);
+        const float top = max3(m, m1, m1);
         scale0 = m == -INFINITY ? 0.f : pa::ex2(m - top);
         scale1 = m1 == -INFINITY ? 0.f : pa::ex2(m1 - top);
         l = l * scale0 + l1 * scale1, m = top;
@@ -805,8 +806,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         tmem_arrived(o);
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = w0 > 0.f ? __uint_as_float(o[i]) * w0 : 0.f;
-        if (w1 > 0.f)
+        for (int i = 0; i < 32; ++i) x[i] = w0 != 0.f ? __uint_as_float(o[i]) * w0 : 0.f;
+        if (w1 != 0.f)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = fmaf(other[(32 * k + i) * kTile + row], w1, x[i]);
         // a thread writes its own row, 64 or 128 bytes a step: whole lines by

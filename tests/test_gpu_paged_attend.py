@@ -281,6 +281,33 @@ def test_a_masked_value_weighs_exactly_nothing(new, dt, slopes):
         check(out.cpu(), lse.cpu(), want, dt, dz, n)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new, n", [(1, 40), (1, 3000), (130, 330), (40, 3000)])
+def test_a_seen_nan_reaches_its_rows_and_no_others(new, n, dt, softcap):
+    """One key element is NaN: the heads of its KV head are NaN in out and lse for the tokens that see it, in whichever
+    tile, run or lane it falls, and every other row is what it is without."""
+    P, Hq = 16, 4
+    for at in (n - 1, n - new + new // 2, 17, 6):
+        toks, pool, table = _cache(1, n, dt=dt)
+        page = int(table[0, at // P])
+        kpool = pool.clone()
+        kpool[page, 0, at % P, 77] = float("nan")
+        q = torch.randn(new, Hq, D, generator=torch.Generator().manual_seed(6)).to(dt)
+        out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+        hkv.hkv_prefill_attend_paged(q.to(DEV), kpool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, status=st,
+                                     softcap=softcap, ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt))
+        assert hkv.hkv_check(st) == hkv.HKV_OK
+        pos, lo, hi = spans(n, new)
+        hit = torch.zeros(new, Hq, dtype=torch.bool)
+        hit[pos >= at, :2] = True
+        assert torch.equal(out.cpu().isnan().all(-1), hit) and torch.equal(out.cpu().isnan().any(-1), hit)
+        assert torch.equal(lse.cpu().isnan(), hit)
+        want = attend(q, toks[0], toks[0], pos, lo, hi, 1 / math.sqrt(D), softcap)
+        o = torch.where(hit[..., None], want[0].to(dt), out.cpu())
+        check(o, torch.where(hit, want[1].float(), lse.cpu()), want, dt, score_error(q, toks[0], 1 / math.sqrt(D)), n)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("new", [1, 60])
 def test_pages_behind_the_window_may_be_gone(new, dt):
