@@ -14,7 +14,10 @@
 // one is finished, so that the eight warps of an SM keep 128 KB on their way
 // without ever waiting for each other.  The work is bound by reading K and V: a
 // 128-row tcgen05 tile would be seven eighths padding, so scores and products
-// are mma.sync with the 16 rows as M.
+// are mma.sync with the 16 rows as M.  64 sequences of up to 8192 tokens (bf16,
+// capped scores) take 269 to 285 us, 5.7 to 6.1 TB/s.  fp32 is bound by the
+// latency of its three dependent products instead: chunks of 37 tokens behind
+// 900 take 26 us.
 //   bf16: m16n8k16; P is rounded to bf16 for the product, sums stay fp32.
 //   fp32: m16n8k8 tf32 in three products.  x = hi + lo, both rounded to tf32's
 //         11 bits; hi hi + hi lo + lo hi leaves out lo lo and the rounding of

@@ -15,6 +15,15 @@
 // the first tiles is rare, so the softmax threads do it themselves.
 // With at most 128 rows both slots take the same rows and every other tile.
 //
+// What bounds it: the products, 2 x 128 x 128 x 256 flops a tile and slot, and
+// beside them as much time of exponentials, which is why a slot weighs scores
+// while the other multiplies.  A causal prompt of 8192 tokens (32 query heads, 8
+// KV heads) takes 465 us, 1.18 PFLOP/s or 71% of a large library product's rate;
+// 256 sequences behind 98304 tokens 376 us, 1.10 PFLOP/s.  With 256 rows of one
+// KV head the tiles' reads (2 x 32 KB for 16.8 MFLOP) stay far below the
+// memory's rate.  Where the rows are few or see little (chunks in a window,
+// short documents) a CTA's start and end, 7.5 us, and its longest row tile show.
+//
 // Warps 0-3 and 4-7: softmax of slot 0 and 1; 8: K tiles, 9: V tiles (TMA boxes
 // of as many tokens as a page's size allows, or plain loads where a page ends
 // inside a swizzle group, at the end of the sequence and at bad pages);
@@ -37,7 +46,7 @@ constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kHalf = kTile * 128;     // 128 rows x 64 bf16
 constexpr uint32_t kBuf = 2 * kHalf;
 constexpr int kMaskRing = 8;                // tiles whose valid-token masks are kept
-constexpr uint32_t kPolyMask = 0x11;        // of eight pairs of exponentials, those taken by the polynomial
+constexpr uint32_t kPolyMask = 0x11;        // of eight pairs of exponentials, the two taken by the polynomial (three: no faster)
 constexpr float kGrowth = 8.f;              // rescale when the maximum grows by more than 2^8
 
 struct Layout {
