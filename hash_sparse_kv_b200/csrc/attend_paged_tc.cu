@@ -893,6 +893,7 @@ int64_t tc_tiles(const PagedAttend& p, bool prefix) {
 // parts at 4 TB/s.  Prompts, whose rows mostly see different lengths, are cut
 // only where they leave SMs idle, down to two tiles.
 int tc_splits(const PagedAttend& p, bool prefix, int sms) {
+  if (sms < 1) sms = 1;  // no device (sizes only), or one whose SMs are all spoken for
   const int64_t ctas = tc_tiles(p, prefix) * p.Hkv;
   if (!prefix) {
     const int64_t most = ceil_div(p.n_max, 2 * kTile);
