@@ -1,6 +1,6 @@
 // Dense attention over a paged cache for few rows at a time: the single-token
 // (decode) form of the prompt attention, the own tokens of sequences behind a
-// shared prefix, and everything in fp32.
+// shared prefix, a short prefix itself, and everything in fp32.
 //
 // An item is up to 16 rows of one KV head (the g query heads of 16 / g new
 // tokens) and one run of their cache positions.  A warp goes through items on
@@ -118,15 +118,13 @@ struct Item {
   int first, last;         // the steps of this run
   pa::Span mine;
 };
-// Items are the runs of the shared prefix first (fp32: rows of all sequences
-// side by side), then those of the sequences' own tokens.
+// Items are the runs of the shared prefix first (rows of all sequences side by
+// side), then those of the sequences' own tokens.
 template <typename T>
 __device__ __forceinline__ Item open_item(const Args& a, int w, bool tell) {
   const int lane = threadIdx.x & 31, tpt = kRows / a.g;
   Item it;
-  // in bf16 the prefix, and sequences of more than 16 rows, go to the
-  // tensor-core kernel
-  const bool prefix = sizeof(T) == 4 && w < a.prefix_items;
+  const bool prefix = w < a.prefix_items;
   if (!prefix) w -= a.prefix_items;
   const int parts = prefix ? a.prefix_parts : a.own_parts, run = w % parts, rest = w / parts;
   it.j = rest % a.Hkv;
@@ -405,11 +403,12 @@ rows_kernel(const __grid_constant__ Args a, int items) {
 
 // Joins the parts of every row: out = sum_p 2^(m_p - M) o_p / L, with M the
 // largest m_p and L = sum_p 2^(m_p - M) l_p.  One warp per row, four columns a
-// lane; the parts' loads are independent of one another.
-template <typename T>
+// lane; kAhead parts' loads are on their way together (four are enough for a few
+// parts; eight take 2.5 us from 64).
+template <typename T, int kAhead>
 __global__ void __launch_bounds__(128)
 join_parts_kernel(const __grid_constant__ Args a) {
-  constexpr int Q = kHeadDim / 4, kAhead = 4;
+  constexpr int Q = kHeadDim / 4;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), n_rows = a.T * a.Hq;
   const int lane = threadIdx.x & 31, parts = a.prefix_parts + a.own_parts;
   bool mine = row < n_rows;
@@ -456,17 +455,29 @@ join_parts_kernel(const __grid_constant__ Args a) {
   if (lane == 0 && a.lse) a.lse[row] = L != 0.f ? (M + log2f(L)) * pa::kLn2 : -INFINITY;
 }
 
-// Runs of positions that an item is cut into.  Few items are cut until every
-// worker has one, down to eight steps; many items only into runs of at least
-// 32 steps, six for every worker, so that the last ones to run are short.
-int splits_for(int64_t items, int64_t tokens, int64_t workers, int step) {
-  auto cut = [&](int64_t want, int64_t least) {
-    want = ceil_div(want, items < 1 ? 1 : items);
-    const int64_t most = ceil_div(tokens, least);
-    return want < most ? want : most;
+// Items of one kind: `n` of them, each over `steps` steps of positions.
+struct Kind {
+  int64_t n, steps;
+  int64_t runs(int64_t length) const { return n > 0 ? ceil_div(steps, length) : 0; }
+};
+
+// Steps of a run: items are cut into runs until every worker has one, down to
+// sqrt(steps / 10): a step alone on its SM takes 0.5 us, joining one more part
+// 0.05 us (single tokens of 8 sequences of 300 tokens: 15.7 us with eight steps a
+// run at least, 10.1 with two; of 1000 tokens: 14.4 us in one wave of 16 runs,
+// 17.9 in a wave and a bit).  Longer work is cut only into runs of at least 32
+// steps, six for every worker, so that the last ones to run are short.
+int64_t run_steps(const Kind& a, const Kind& b, int64_t workers) {
+  const int64_t longest = a.steps > b.steps ? a.steps : b.steps;
+  auto fits = [&](int64_t length, int64_t most) {
+    while (length < longest && a.n * a.runs(length) + b.n * b.runs(length) > most) length += length / 8 + 1;
+    return length;
   };
-  const int64_t few = cut(workers, 8 * step), many = cut(6 * workers, 32 * step), s = few > many ? few : many;
-  return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  int64_t least = 2;
+  while (10 * least * least < longest) ++least;
+  const int64_t few = fits(least, workers), many = fits(32, 6 * workers), most_runs = ceil_div(longest, 64);
+  const int64_t r = few < many ? few : many;
+  return r > most_runs ? r : most_runs;
 }
 
 // How a call is cut up; from its shape and the device alone, so that the
@@ -475,7 +486,7 @@ struct Plan {
   bool tc = false;         // prompts: the tensor-core kernel takes all rows
   int64_t own_items = 0;   // rows of one sequence (16 at most), all KV heads together
   int prefix_parts = 0, own_parts = 1;
-  int prefix_items = 0;    // fp32: runs of the prefix that the same kernel takes
+  int prefix_items = 0;    // runs of the prefix that this file's kernel takes
   int row_ctas = 0;        // blocks of this file's kernel, one per SM
   int parts = 0;           // a row's partial results, 0 when its block finishes it
   size_t o = 0, total = 0;  // byte offset of part_o behind part_ml, and the size
@@ -491,23 +502,33 @@ Plan plan(const PagedAttend& p) {
     r.own_parts = tc_splits(p, false, sms);
   } else {
     r.own_items = (int64_t)p.B * ceil_div(p.max_q, tpt) * p.Hkv;
-    r.own_parts = splits_for(r.own_items, p.n_max, kWarps * sms, bf16 ? kStep<__nv_bfloat16> : kStep<float>);
-    int64_t items = r.own_items * r.own_parts;
-    if (p.n_prefix > 0 && !bf16) {
-      const int64_t tiles = ceil_div(p.B, tpt) * p.Hkv;
-      r.prefix_parts = splits_for(tiles, p.n_prefix, kWarps * sms, kStep<float>);
-      r.prefix_items = (int)(tiles * r.prefix_parts);
-      items += r.prefix_items;
-    }
+    const int step = bf16 ? kStep<__nv_bfloat16> : kStep<float>;
+    const int64_t workers = (int64_t)kWarps * sms;
+    const Kind own{r.own_items, p.n_max > 0 ? ceil_div(p.n_max, step) : 1};
+    Kind prefix{p.n_prefix > 0 ? ceil_div(p.B, tpt) * p.Hkv : 0, ceil_div(p.n_prefix, step)};
+    // A short prefix goes the way of the own tokens, in bf16 too: one launch
+    // less, and no CTA's start and end (8 sequences behind 400 tokens 9.6 us
+    // instead of 11.9, 32 behind 256 11.3 instead of 15.2; 32 behind 2000, which
+    // are read for every 16 rows again, 27 instead of 19).
+    const bool tc_prefix = prefix.n > 0 && bf16 && (p.n_prefix > 1024 || prefix.n * prefix.steps > 4 * workers);
+    if (tc_prefix) prefix = Kind{0, 0};
+    // beside the prefix's kernel, on fewer SMs, twice as many runs keep the
+    // warps busy to the end (16 sequences of up to 2000 tokens behind 32768:
+    // 68 us, 56 with twice as many)
+    const int64_t length = run_steps(own, prefix, tc_prefix ? 2 * workers : workers);
+    r.own_parts = (int)own.runs(length);
+    r.prefix_parts = (int)prefix.runs(length);
+    r.prefix_items = (int)(prefix.n * r.prefix_parts);
+    const int64_t items = r.own_items * r.own_parts + r.prefix_items;
     r.row_ctas = (int)(items < sms ? items : sms);
-    if (p.n_prefix > 0 && bf16) {
+    if (tc_prefix) {
       // The prefix (bound by the tensor cores) and the sequences' own tokens
       // (bound by memory) run side by side on SMs of their own, shared out by
       // the time that each would take of one SM: 1.75 us for a tile of 128
       // tokens and 256 rows, 45 GB/s and 0.5 us an item for the own tokens,
       // taken to be half as long as they may be.  (64 sequences of up to 512
-      // tokens behind 32768: one after the other 73 us, side by side 63 us; 256
-      // of up to 128 behind 98304: 409 and 375 us.)
+      // tokens behind 32768: one after the other 73 us, side by side 63 to 66;
+      // 256 of up to 128 behind 98304: 409 and 375 us.)
       const double prefix_us = 1.75 * (double)tc_tiles(p, true) * p.Hkv * (double)ceil_div(p.n_prefix, 128);
       const double own_us = (double)p.B * p.Hkv * (double)p.n_max * 0.5 * 512 / 45e3 + 0.5 * (double)items;
       const int share = (int)(sms * own_us / (own_us + prefix_us) + 0.5);
@@ -536,10 +557,11 @@ int run(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
     if (rc != HKV_OK) return rc;
     kernel<<<pl.row_ctas, kWarps * 32, kRingBytes, st>>>(a, (int)items);
     rc = cuda_check(cudaGetLastError(), "paged attention launch");
-    if (rc == HKV_OK && sizeof(T) == 2 && pl.prefix_parts > 0) rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
+    if (rc == HKV_OK && pl.prefix_parts > 0 && pl.prefix_items == 0) rc = launch_attend_tc(p, a, true, pl.prefix_parts, 0, st);
   }
   if (rc != HKV_OK || pl.parts == 0) return rc;
-  return cuda_check(launch_after(join_parts_kernel<T>, dim3((unsigned)ceil_div(a.T * a.Hq, 4)), 128, 0, st, a),
+  auto join = pl.parts > 4 ? join_parts_kernel<T, 8> : join_parts_kernel<T, 4>;
+  return cuda_check(launch_after(join, dim3((unsigned)ceil_div(a.T * a.Hq, 4)), 128, 0, st, a),
                     "attention join launch");
 }
 

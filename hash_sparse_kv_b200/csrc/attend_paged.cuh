@@ -43,7 +43,7 @@ struct Args {
   float* part_o;
   float2* part_ml;            // running maximum (log2 units) and sum
   int prefix_parts, own_parts;
-  int prefix_items;           // items of the prefix that the row kernel takes (fp32)
+  int prefix_items;           // items of the prefix that the row kernel takes
   int32_t* status;
   uint64_t wait_ns;
 };
