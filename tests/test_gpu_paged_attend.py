@@ -476,3 +476,24 @@ def test_from_prompt_to_retrieval():
         assert (full[b].cpu().double() - want[0][0]).abs().max() < 2e-3 and (lse2[b].cpu().double() - want[1][0]).abs().max() < 2e-3
         if b == 0:
             check(out3.cpu(), lse3.cpu(), want, BF, dz, m)
+
+
+LONGER = [
+    # prefixes that the 128-row tiles read, and those at the border to the 16-row ones
+    (BF, 8, 2, 48, 1777, list(range(1, 71)), {}),
+    (BF, 8, 8, 5, 1303, [9, 10], dict(softcap=10.0, spread=4.0)),
+    (BF, 2, 2, 1, 1131, [3] * 200, {}),
+    (BF, 28, 4, 64, 1100, [70] * 90, dict(slopes=True)),
+    (BF, 8, 2, 16, 1024, [0, 0], {}),
+    (BF, 8, 2, 16, 1025, [0, 0], {}),
+    (BF, 8, 8, 16, 900, [2] * 300, {}),
+    (BF, 6, 2, 100, 1500, [1, 0, 400], dict(strided=True)),
+    (BF, 16, 1, 32, 1, [1, 2, 0], {}),
+    (BF, 3, 1, 24, 17, [1] * 40, dict(softcap=5.0, slopes=True, spread=4.0)),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONGER)))
+def test_shared_prefix_on_either_kernel(case):
+    dt, Hq, Hkv, P, n_prefix, own, kw = LONGER[case]
+    _shared(dt, Hq, Hkv, P, n_prefix, own, seed=700 + case, **kw)
