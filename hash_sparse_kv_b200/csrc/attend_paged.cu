@@ -238,7 +238,7 @@ rows_kernel(const __grid_constant__ Args a, int items) {
     constexpr int kLine = 128 / (int)sizeof(T);
     const void* at = lane == 0 ? static_cast<const void*>(a.pm.table + (int64_t)b * a.pm.max_pages)
                                : static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)j * a.g * D + (lane - 1) * kLine;
-    if (lane == 0 || (lane <= a.g * D / kLine && tok >= 0 && tok < a.T)) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    if (lane == 0 ? a.pm.max_pages > 0 : lane <= a.g * D / kLine && tok >= 0 && tok < a.T) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
   };
   call_in(worker);
   call_in(worker + workers);

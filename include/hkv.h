@@ -563,9 +563,9 @@ int hkv_prefill_attend_paged(int B, int64_t T, int Hq, int Hkv, int dtype, const
 size_t hkv_prefill_workspace_bytes(int B, int64_t T, int Hq, int Hkv, int dtype, int max_q, int64_t n_tokens_max);
 
 /* Dense decode step of a batch of sequences that share their first n_prefix
- * tokens.  The prefix's keys and values are read once for the whole batch: the
- * query heads of all sequences meet them together, and the result is joined
- * with each sequence's own tokens by log-sum-exp rescaling.
+ * tokens.  The prefix's keys and values are read from memory once for the whole
+ * batch: the query heads of all sequences meet them together, and the result is
+ * joined with each sequence's own tokens by log-sum-exp rescaling.
  * Sequence b is the prefix, in the pages prefix_table[0 ..], then its own
  * n_own_b[b] tokens, in the pages page_table[b, 0 ..] of the same pools (its own
  * tokens start on a page of their own; the prefix may end inside a page).  Its

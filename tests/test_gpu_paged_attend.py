@@ -497,3 +497,50 @@ LONGER = [
 def test_shared_prefix_on_either_kernel(case):
     dt, Hq, Hkv, P, n_prefix, own, kw = LONGER[case]
     _shared(dt, Hq, Hkv, P, n_prefix, own, seed=700 + case, **kw)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [1, 40])
+def test_caches_without_a_page(new, dt):
+    """Page tables with no columns: nothing is seen, and behind a prefix only the prefix."""
+    Hq, Hkv, P, B = 8, 2, 16, 3
+    pool = torch.randn(90, Hkv, P, D, device=DEV).to(dt)
+    table = torch.zeros(B, 0, dtype=torch.int32, device=DEV)
+    T = B * new
+    q = torch.randn(T, Hq, D, device=DEV).to(dt)
+    out, lse, st = torch.ones(T, Hq, D, dtype=dt, device=DEV), torch.ones(T, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q, pool, pool, table, _i([new * b for b in range(B + 1)]), _i([0] * B), new, 0, out, lse=lse,
+                                 ws=hkv.prefill_workspace(B, Hq, Hkv, T, new, 0, dt), status=st)
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    assert (out == 0).all() and (lse == -math.inf).all()
+    if new > 1:
+        return
+    for n in (40, 1300):
+        pages = torch.arange(-(-n // P), dtype=torch.int32, device=DEV)
+        hkv.hkv_shared_attend_paged(q, pool, pool, pages, n, table, _i([0] * B), 0, out, lse=lse, status=st,
+                                    ws=hkv.shared_workspace(B, Hq, Hkv, n, 0, dt))
+        assert hkv.hkv_check(st) == hkv.HKV_OK
+        K = pool.cpu().transpose(1, 2).reshape(-1, Hkv, D)[:n]
+        for b in range(B):
+            want = attend(q[b:b + 1].cpu(), K, K, torch.tensor([n - 1]), torch.tensor([0]), torch.tensor([n]), 1 / math.sqrt(D))
+            check(out[b:b + 1].cpu(), lse[b:b + 1].cpu(), want, dt, score_error(q[b:b + 1].cpu(), K, 1 / math.sqrt(D)), n)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_drawn_batches(seed):
+    """Ragged batches, heads, pages and masks drawn together."""
+    import random
+    r = random.Random(seed)
+    Hq, Hkv = r.choice([(4, 2), (28, 4), (16, 16), (12, 4), (5, 1)])
+    dt = r.choice([BF, BF, F32])
+    B = r.randint(1, 9)
+    top = r.choice([1, 3, 40, 170])
+    new = [r.randint(0, top) for _ in range(B)]
+    total = [max(1, n + r.randint(0, r.choice([0, 30, 900]))) for n in new]
+    if not sum(new):
+        new[0] = 1
+    _prompt(dt, Hq, Hkv, r.choice([1, 7, 16, 40, 64, 128]), new, total, softcap=r.choice([0.0, 20.0]),
+            window=r.choice([0, 0, 1, 90]), slopes=r.random() < 0.3, docs=r.choice([0, 0, 50]),
+            prefix=[r.randint(0, 200) for _ in range(B)] if r.random() < 0.3 else None, spread=3.0, seed=900 + seed)
+    _shared(dt, Hq, Hkv, r.choice([3, 16, 48, 64]), r.choice([1, 200, 1024, 1100, 2500]), [r.randint(0, 80) for _ in range(B)] + [1],
+            softcap=r.choice([0.0, 20.0]), slopes=r.random() < 0.3, seed=950 + seed, spread=3.0)
