@@ -33,16 +33,19 @@
 #include <type_traits>
 
 #include "attend_paged.cuh"
+#include "attend_paged_turns.h"
 #include "tc.cuh"
 
 namespace hkv {
 namespace {
 
 using pa::Args;
+using pa::kKStages;
+using pa::kVStages;
+using pa::Run;
 
 constexpr int kThreads = 384;
 constexpr int kTile = 128;                  // tokens per tile, rows per slot
-constexpr int kKStages = 3, kVStages = 2;
 constexpr uint32_t kHalf = kTile * 128;     // 128 rows x 64 bf16
 constexpr uint32_t kBuf = 2 * kHalf;
 constexpr int kMaskRing = 8;                // tiles whose valid-token masks are kept
@@ -342,12 +345,6 @@ struct Loader {
   }
 };
 
-// A slot's tiles: every step-th from first up to last.
-struct Run {
-  int first, last, step;
-  __device__ __forceinline__ int count() const { return last > first ? (last - first + step - 1) / step : 0; }
-};
-
 // How scores are formed: scaled only; capped too; with a bias by distance (and
 // a cap or a scale of any sign).
 enum { kPlain = 0, kCapped = 1, kBiased = 2 };
@@ -603,8 +600,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
     float m = -INFINITY, l = 0.f;
     int done = 0;  // tiles that this slot has been through
-    const Run run = run_of(slot), other_run = run_of(1 - slot);
-    const int turns = min(run.count(), other_run.count());  // tiles for which the slots take turns
+    const Run run = run_of(slot);
+    const pa::Turns turns = pa::turns_of(run, run_of(1 - slot), both);
     // a score in units of log2(e) is value * c: value is q.k, or its tanh, or
     // (biased) the score itself
     const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f, cap = a.softcap * pa::kLog2e;
@@ -708,8 +705,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       // One slot's exponentials at a time: together they would take as long, and
       // the tensor cores would wait for both instead of working for the other.
-      if (done < turns && (slot == 1 || done > 0)) {
-        const bool ok3 = wait(&turn[slot], (slot == 1 ? done : done - 1) & 1, abort, a.wait_ns);
+      const bool in_turn = turns.has(done);
+      if (in_turn && (slot == 1 || done > turns.from)) {
+        const bool ok3 = wait(&turn[slot], (done - turns.from - (slot == 1 ? 0 : 1)) & 1, abort, a.wait_ns);
         if (!__all_sync(0xffffffffu, ok3)) break;
       }
       const float off = m == -INFINITY ? 0.f : m;
@@ -759,7 +757,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       const float2 both_sums = unpair(add2(sum[0], sum[1]));
       l += both_sums.x + both_sums.y;
       __syncwarp();
-      if (done < turns && lane == 0) tc::mbar_arrive(&turn[1 - slot]);
+      if (in_turn && lane == 0) tc::mbar_arrive(&turn[1 - slot]);
       tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
