@@ -19,9 +19,9 @@
 // latency of its three dependent products instead: chunks of 37 tokens behind
 // 900 take 26 us.
 //   bf16: m16n8k16; P is rounded to bf16 for the product, sums stay fp32.
-//   fp32: m16n8k8 tf32 in three products.  x = hi + lo, both rounded to tf32's
-//         11 bits; hi hi + hi lo + lo hi leaves out lo lo and the rounding of
-//         lo, each 2^-24 of a product at most, as much as fp32's own rounding.
+//   fp32: m16n8k8 tf32 in three products.  x = hi + lo, both of tf32's 11 bits;
+//         hi hi + hi lo + lo hi leaves out lo lo and the rounding of lo, each
+//         2^-22 of a product at most and without a sign of its own.
 #include <cstdio>
 
 #include "attend_paged.cuh"
@@ -76,12 +76,15 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Both parts rounded to the nearest tf32 (half a step is added, and the bits
-// below are dropped here or by the instruction): dropping bits of hi alone
-// would leave errors of one sign.
+// hi is x rounded to the nearest tf32 (half a step is added, the bits below are
+// dropped): dropping bits alone would leave errors of one sign.  The bits of lo
+// below tf32 are dropped by the instruction, so it is taken a third of a step
+// per unit of its mantissa larger first, half a step on average.  That addition
+// is a multiplication: where x is a NaN (or infinite) hi may be anything, its
+// bits having carried into the sign, but x - hi is a NaN, and has to stay one.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint((x - __uint_as_float(hi)) * (1.f + 0x1p-10f / 3.f));
 }
 // d += a b for fp32 a (16 x 8) and b (8 x 8).
 __device__ __forceinline__ void mma_fp32(float (&d)[4], const float (&a)[4], float b0, float b1) {

@@ -520,8 +520,9 @@ size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv
  *               and q_first let them), also by the earlier ones
  *   q_first     nullable, device int32 [T]: the first position that a query
  *               sees, e.g. the start of its document
- * Keys that a query does not see may hold anything; a NaN in one that it sees
- * makes its out and lse NaN.  Values must be finite (fp32: below 2^128 - 2^116)
+ * Keys that a query does not see may hold anything; a NaN in one that it sees,
+ * or in the query, whatever its bits, makes its out and lse NaN, and so does an
+ * infinity in fp32.  Values must be finite (fp32: below 2^128 - 2^116)
  * at every position below n: one that some query of the sequence sees is also
  * multiplied, by zero, for the others. */
 typedef struct {

@@ -308,6 +308,56 @@ def test_a_seen_nan_reaches_its_rows_and_no_others(new, n, dt, softcap):
         check(o, torch.where(hit, want[1].float(), lse.cpu()), want, dt, score_error(q, toks[0], 1 / math.sqrt(D)), n)
 
 
+@pytest.mark.parametrize("dt, bits", [(F32, b) for b in (0x7fffffff, 0xffffffff, 0x7ffff000, 0xfffff000, 0x7f800001, 0xff800fff,
+                                                        0x7fbfffff)] + [(BF, b) for b in (0x7fff, 0xffff, 0x7f81, 0xff81)])
+@pytest.mark.parametrize("new, n", [(1, 3000), (40, 300)])
+def test_every_bit_pattern_of_nan_is_one(new, n, dt, bits):
+    """Arithmetic on a GPU writes NaN as 0x7fffffff; a payload may be anything.  In a key or in a query."""
+    Hq, at = 4, n - new // 2 - 1
+    wide, word = (torch.int32, 1 << 32) if dt == F32 else (torch.int16, 1 << 16)
+    nan = torch.tensor(bits - word if bits >= word // 2 else bits, dtype=wide).view(dt)
+    assert nan.isnan()
+    toks, pool, table = _cache(1, n, dt=dt)
+    q = torch.randn(new, Hq, D, generator=torch.Generator().manual_seed(6)).to(dt).to(DEV)
+    pos, lo, hi = spans(n, new)
+    want = attend(q.cpu(), toks[0], toks[0], pos, lo, hi, 1 / math.sqrt(D))
+    for in_key in (True, False):
+        kpool, qn = pool.clone(), q.clone()
+        hit = torch.zeros(new, Hq, dtype=torch.bool)
+        if in_key:
+            kpool.view(wide)[int(table[0, at // 16]), 1, at % 16, 5] = nan.view(wide)
+            hit[pos >= at, 2:] = True
+        else:
+            qn.view(wide)[new // 2, 1, 90] = nan.view(wide)
+            hit[new // 2, 1] = True
+        out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+        hkv.hkv_prefill_attend_paged(qn, kpool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, status=st,
+                                     ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt))
+        assert hkv.hkv_check(st) == hkv.HKV_OK
+        assert torch.equal(out.cpu().isnan().all(-1), hit) and torch.equal(out.cpu().isnan().any(-1), hit)
+        assert torch.equal(lse.cpu().isnan(), hit)
+        o = torch.where(hit[..., None], want[0].to(dt), out.cpu())
+        check(o, torch.where(hit, want[1].float(), lse.cpu()), want, dt, score_error(q.cpu(), toks[0], 1 / math.sqrt(D)), n)
+
+
+def test_a_nan_that_the_append_turned_is_still_one():
+    """fp32: appended with a NaN, turned by its position, seen by every later token."""
+    n, Hq, at = 50, 2, 20
+    g = torch.Generator().manual_seed(8)
+    k = torch.randn(n, 1, D, generator=g).to(DEV)
+    k[at, 0, 3] = float("nan")
+    K, V = (torch.zeros(4, 1, 16, D, device=DEV) for _ in range(2))
+    table, q = _i([[2, 0, 3, 1]]), torch.randn(n, Hq, D, generator=g).to(DEV)
+    inv = (1e4 ** (-torch.arange(64) / 64)).float().to(DEV)
+    hkv.hkv_append_paged(None, k, torch.randn(n, 1, D, generator=g).to(DEV), K, V, table, _i([0, n]), _i([0]),
+                         rope=hkv.RopeParams(inv), q=q, q_out=q)
+    out, lse = torch.zeros(n, Hq, D, device=DEV), torch.zeros(n, Hq, device=DEV)
+    hkv.hkv_prefill_attend_paged(q, K, V, table, _i([0, n]), _i([n]), n, n, out, lse=lse,
+                                 ws=hkv.prefill_workspace(1, Hq, 1, n, n, n, F32))
+    assert torch.equal(lse.isnan().all(1).cpu(), torch.arange(n) >= at)
+    assert torch.equal(out.isnan().all(-1).all(1).cpu(), torch.arange(n) >= at)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("new", [1, 60])
 def test_pages_behind_the_window_may_be_gone(new, dt):
