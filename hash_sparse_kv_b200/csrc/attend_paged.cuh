@@ -70,15 +70,14 @@ struct Span {
   int lo, hi, pos;
 };
 // Positions seen by new token i of sequence b, whose pages hold all of it.
-// `docs`: whether q_first counts.
-__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i, bool docs = true) {
+__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int b, int64_t i) {
   Span r;
   // more new tokens than the sequence has: positions below zero see nothing but
   // a prefix
   const int64_t p = s.n - s.n_new + i;
   int64_t lo = 0, hi = p + 1;
   if (a.window > 0 && p + 1 - a.window > lo) lo = p + 1 - a.window;
-  if (docs && a.q_first) {
+  if (a.q_first) {
     const int64_t f = a.q_first[s.first + i];
     lo = f > lo ? f : lo;
   }

@@ -58,7 +58,8 @@ struct Layout {
   static constexpr uint32_t kV = kK + kKStages * kBuf;
   static constexpr uint32_t kMask = kV + kVStages * kBuf;
   static constexpr uint32_t kBars = kMask + kMaskRing * 16;
-  static constexpr uint32_t kEnd = kBars + 256;
+  static constexpr uint32_t kSeen = kBars + 256;
+  static constexpr uint32_t kEnd = kSeen + 64;
 };
 constexpr size_t kSmem = 1024 + Layout::kEnd;
 
@@ -273,6 +274,10 @@ struct Loader {
   const int32_t* __restrict__ table;
   int n_tok, j;              // tokens behind the table, KV head
   int lo, hi;                // positions that some row sees: the places of others need not exist
+  // tiles that start before this position are not read whole.  What lies before
+  // the first seen position, in the page that the table names for it, may be
+  // NaN; a key's score is masked then, but a weight of zero does not undo a value
+  int least;
   int32_t rows[4];           // pool rows of tokens lane, lane + 32, + 64, + 96 of a tile, -1: none
   uint64_t* pending = nullptr;  // the barrier of the tile whose copies have not been waited for
 
@@ -301,7 +306,7 @@ struct Loader {
     if (t.box > 0) {
       const int boxes = kTile / t.box;  // at most 16
       int32_t row = 0;
-      bool ok = (n + 1) * kTile <= n_tok;
+      bool ok = n * kTile >= least && (n + 1) * kTile <= n_tok;
       if (ok && lane < boxes) {
         row = (int32_t)pa::pool_row(t.a, table, n * kTile + lane * t.box, j);
         ok = row >= 0;
@@ -359,6 +364,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint4* valid_s = reinterpret_cast<uint4*>(smem + Layout::kMask);
+  int2* seen_s = reinterpret_cast<int2*>(smem + Layout::kSeen);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Layout::kBars);
   uint64_t* k_full = bars;                    // [kKStages]
   uint64_t* k_empty = k_full + kKStages;
@@ -403,37 +409,55 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   }
   if (warp == 10) tc::tmem_alloc(tmem_slot, 512);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes next may take the SMs that are free
-  // What a slot's rows see together, a bound rather than the exact union:
-  // positions grow with the rows.  Every warp works it out for itself.
+  // What the softmax threads' rows see, and from the first position to the last
+  // what their warps do.
   const int g = a.g, row_base = (int)r0;  // r0 + 255 < T * g < 2^31
-  auto seen_by = [&](int s, int& lo, int& hi) {
+  const int row = both ? threadIdx.x : (threadIdx.x & (kTile - 1));
+  const bool live = warp < 8 && row < nrows;
+  const int tok = (row_base + row) / g;  // new token within its sequence
+  pa::Span sp{0, INT32_MAX, 0};  // rows that are only padding see everything: no masks for their sake
+  if (live) {
     if constexpr (kPrefix) {
-      lo = 0, hi = (int)a.n_prefix;
+      const int64_t n = min((int64_t)max(a.n_tok[tok], 0), a.n_max);
+      sp = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
     } else {
-      const int ra = both ? s * kTile : 0, rb = min(nrows, ra + kTile) - 1;
-      const int ia = (row_base + ra) / g, ib = (row_base + rb) / g;
-      const pa::Span x = pa::span_of(a, seq, b, ia, false), y = pa::span_of(a, seq, b, ib, false);
-      lo = x.lo, hi = y.hi;
-      if (a.q_first) {
-        int f = INT32_MAX;
-        for (int i = ia + lane; i <= ib; i += 32) f = min(f, __ldg(a.q_first + seq.first + i));
-        lo = max(lo, __reduce_min_sync(0xffffffffu, f));
-      }
+      sp = pa::span_of(a, seq, b, tok);
+    }
+  }
+  if (!kPrefix && warp < 8) {
+    const bool sees = live && sp.lo < sp.hi;
+    const int lo = __reduce_min_sync(0xffffffffu, sees ? sp.lo : INT32_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, sees ? sp.hi : 0);
+    if (lane == 0) seen_s[warp] = make_int2(lo, hi);
+  }
+  const int n_all = kPrefix ? (int)a.n_prefix : (int)seq.n;
+  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)b * a.pm.max_pages;
+  if (warp == 8 && lane < 8) {  // the page ids of the first tiles (about), while the barriers are set up
+    const int from = kPrefix ? 0 : pa::span_of(a, seq, b, row_base / g).lo / kTile;
+    const int to = ((kPrefix ? n_all : pa::span_of(a, seq, b, (row_base + nrows - 1) / g).hi) + kTile - 1) / kTile;
+    const int at = from + split * ((max(to - from, 0) + t.splits - 1) / t.splits) + lane;
+    if (at < to) asm volatile("prefetch.global.L2 [%0];" ::"l"(table + (uint32_t)at * kTile / (uint32_t)a.pm.page_size));
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  auto seen_by = [&](int s, int& lo, int& hi) {
+    lo = 0, hi = n_all;
+    if constexpr (!kPrefix) {
+      const int2* w = seen_s + (both ? 4 * s : 0);
+      lo = min(min(w[0].x, w[1].x), min(w[2].x, w[3].x)), hi = max(max(w[0].y, w[1].y), max(w[2].y, w[3].y));
       lo = min(lo, hi);
     }
   };
   int lo0, hi0, lo1, hi1;
   seen_by(0, lo0, hi0);
   seen_by(1, lo1, hi1);
-  const int n_all = kPrefix ? (int)a.n_prefix : (int)seq.n;
-  const int32_t* table = kPrefix ? a.prefix_table : a.pm.table + (int64_t)b * a.pm.max_pages;
   // tiles of the CTA, then this split's run of them
   const int lo = hi0 <= lo0 ? lo1 : hi1 <= lo1 ? lo0 : min(lo0, lo1), hi = max(hi0 > lo0 ? hi0 : 0, hi1 > lo1 ? hi1 : 0);
   const int first = lo < hi ? lo / kTile : 0, last = lo < hi ? (hi + kTile - 1) / kTile : 0;
   const int per = (last - first + t.splits - 1) / t.splits;
   const int t0 = first + split * per, t1 = min(last, t0 + per);
-  if (warp == 8 && lane < 8 && t0 + lane < t1)  // the page ids of the first tiles, while the barriers are set up
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(table + (uint32_t)(t0 + lane) * kTile / (uint32_t)a.pm.page_size));
   // the tiles that a slot works on
   auto run_of = [&](int s) -> Run {
     if (!both) return Run{t0 + s, t1, 2};
@@ -441,10 +465,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     if (h <= l) return Run{t1, t1, 1};
     return Run{max(t0, l / kTile), min(t1, (h + kTile - 1) / kTile), 1};
   };
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
 
   // The softmax threads hold a row's 128 scores: of the launch's 384 x 168
   // registers 2 x 128 x 200 go to them, 128 x 104 stay with the others.
@@ -458,7 +478,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       unsigned char* ring = smem + (is_k ? Layout::kK : Layout::kV);
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       if (t.box > 0 && lane == 0) tc::tma_prefetch_map(map);
-      Loader ld{t, is_k ? a.K : a.V, map, table, n_all, j, lo, hi, {-1, -1, -1, -1}};
+      Loader ld{t, is_k ? a.K : a.V, map, table, n_all, j, lo, hi, is_k ? 0 : lo, {-1, -1, -1, -1}};
       if (t.box == 0 && t0 < t1) ld.look(t0);
       int stage = 0, armed = 0;
       uint32_t phase = 0;
@@ -563,9 +583,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---------------- softmax: one row per thread ----------------
-    const int slot = warp >> 2, row = both ? threadIdx.x : (threadIdx.x & (kTile - 1));
-    const bool active = (both ? warp : warp & 3) * 32 < nrows, live = row < nrows;
-    const int tok = (row_base + row) / g, head = (row_base + row) % g;  // new token within its sequence
+    const int slot = warp >> 2, head = (row_base + row) % g;
+    const bool active = (both ? warp : warp & 3) * 32 < nrows;
     const int64_t my_out = (seq.first + tok) * a.Hq + j * g + head;     // row of out
     if (active && (both || slot == 0)) {
       // queries to shared memory, two rows at a time
@@ -586,15 +605,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&q_full[slot]);
     }
-    pa::Span sp{0, INT32_MAX, 0};  // rows that are only padding see everything: no masks for their sake
-    if (live) {
-      if constexpr (kPrefix) {
-        const int64_t n = min((int64_t)max(a.n_tok[tok], 0), a.n_max);
-        sp = pa::Span{0, (int)a.n_prefix, (int)(a.n_prefix + n - 1)};
-      } else {
-        sp = pa::span_of(a, seq, b, tok, true);
-      }
-    }
     // tiles within [all_lo, all_hi) are seen whole by every row of the warp
     const int all_lo = __reduce_max_sync(0xffffffffu, sp.lo), all_hi = __reduce_min_sync(0xffffffffu, sp.hi);
     const uint32_t s_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + slot * 256, o_tmem = s_tmem + kTile;
@@ -602,6 +612,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     int done = 0;  // tiles that this slot has been through
     const Run run = run_of(slot);
     const pa::Turns turns = pa::turns_of(run, run_of(1 - slot), both);
+    int at_turn = -turns.from;
     // a score in units of log2(e) is value * c: value is q.k, or its tanh, or
     // (biased) the score itself
     const float to_cap = a.softcap > 0.f ? a.scale / a.softcap : 0.f, cap = a.softcap * pa::kLog2e;
@@ -705,9 +716,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       // One slot's exponentials at a time: together they would take as long, and
       // the tensor cores would wait for both instead of working for the other.
-      const bool in_turn = turns.has(done);
-      if (in_turn && (slot == 1 || done > turns.from)) {
-        const bool ok3 = wait(&turn[slot], (done - turns.from - (slot == 1 ? 0 : 1)) & 1, abort, a.wait_ns);
+      const bool in_turn = (unsigned)at_turn < (unsigned)turns.n;
+      if (in_turn && (slot == 1 || at_turn > 0)) {
+        const bool ok3 = wait(&turn[slot], (slot == 1 ? at_turn : at_turn - 1) & 1, abort, a.wait_ns);
         if (!__all_sync(0xffffffffu, ok3)) break;
       }
       const float off = m == -INFINITY ? 0.f : m;
@@ -762,7 +773,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&p_full[slot]);
-      ++done;
+      ++done, ++at_turn;
     }
     if (done > 0) {
       const bool ok = wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);

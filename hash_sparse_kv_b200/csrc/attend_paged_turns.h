@@ -26,7 +26,6 @@ struct Run {
 // the slot's own tile number `from`.
 struct Turns {
   int from, n;
-  HKV_BOTH_SIDES bool has(int done) const { return done >= from && done < from + n; }
 };
 
 // Slots that share every tile take turns on the tiles that both work on.  Their

@@ -523,8 +523,9 @@ size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv
  * Keys that a query does not see may hold anything; a NaN in one that it sees,
  * or in the query, whatever its bits, makes its out and lse NaN, and so does an
  * infinity in fp32.  Values must be finite (fp32: below 2^128 - 2^116)
- * at every position below n: one that some query of the sequence sees is also
- * multiplied, by zero, for the others. */
+ * from the first position that some query of the sequence sees up to n: one
+ * that a query sees is also multiplied, by zero, for others.  What lies before
+ * that position may hold anything, the page table's entries included. */
 typedef struct {
   float softcap;
   int32_t window;

@@ -376,6 +376,43 @@ def test_pages_behind_the_window_may_be_gone(new, dt):
     check(out.cpu(), lse.cpu(), want, dt, score_error(q.cpu(), K, 1 / math.sqrt(D)), n)
 
 
+@pytest.mark.parametrize("P", [5, 16, 64, 128])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [1, 60, 300])
+@pytest.mark.parametrize("mask", ["window", "documents", "both"])
+def test_pages_before_the_first_seen_position_may_hold_anything(mask, new, dt, P):
+    """A cache that gives back the pages it has left and does not tidy its table: the entries name pages that are someone
+    else's by now, here ones of NaN.  What lies before the first seen position in a page that stays may be NaN too."""
+    n, Hq = 1000, 4
+    toks, pool, table = _cache(1, n, P=P, dt=dt)
+    pos = torch.arange(n - new, n)
+    window, first = 0, None
+    if mask == "window":
+        window = 171
+    elif mask == "documents":
+        first = torch.full((new,), n - new - 90)
+    else:  # the window's start grows, the documents' falls: the first seen position is in the middle of the rows
+        window, first = 400, torch.maximum(n - 700 - 2 * torch.arange(new), torch.tensor(3))
+    _, lo, hi = spans(n, new, window, 0, first)
+    least = int(lo[lo < hi].min())
+    K = toks[0].clone()
+    K[:least] = float("nan")
+    spare = next(p for p in range(pool.shape[0]) if p not in table[0].tolist())
+    pool[spare] = float("nan")
+    for i, page in enumerate(table[0, :-(-n // P)].tolist()):
+        rows = K[i * P:(i + 1) * P]
+        pool[page, :, :len(rows)] = rows.transpose(0, 1).to(DEV)
+    table[0, :least // P] = spare
+    q = torch.randn(new, Hq, D, generator=torch.Generator().manual_seed(9)).to(dt)
+    out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q.to(DEV), pool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, window=window,
+                                 q_first=None if first is None else first.int().to(DEV), status=st,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt))
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    want = attend(q, toks[0], toks[0], pos, lo, hi, 1 / math.sqrt(D))
+    check(out.cpu(), lse.cpu(), want, dt, score_error(q, toks[0], 1 / math.sqrt(D)), n)
+
+
 def test_sequences_may_share_pages_and_calls_may_overlap():
     """The same pages in two sequences' tables, and two calls on two streams with a workspace each."""
     n, Hq, new = 900, 8, 40
