@@ -490,6 +490,9 @@ static int check_attend(int B, int64_t T, int Hq, int Hkv, int dtype, float scal
   p.B = B, p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.dtype = dtype, p.scale = scale;
   if (score != nullptr) {
     if (!std::isfinite(score->softcap) || score->softcap < 0.f) return fail(HKV_ERR_INVALID_ARG, "softcap %f", (double)score->softcap);
+    // beyond these the scores' factors, and powers of them, leave fp32's range
+    if (score->softcap > 0x1p100f || (score->softcap > 0.f && std::fabs(scale) > 0x1p16f * score->softcap))
+      return fail(HKV_ERR_UNSUPPORTED, "softcap %g with scale %g", (double)score->softcap, (double)scale);
     if (score->window < 0) return fail(HKV_ERR_INVALID_ARG, "window %d", score->window);
     p.softcap = score->softcap, p.window = score->window, p.slopes = score->slopes;
     p.prefix_len = score->prefix_len, p.q_first = score->q_first;

@@ -162,7 +162,12 @@ __device__ __forceinline__ Item open_item(const Args& a, int w, bool tell) {
   return it;
 }
 
-template <typename T, bool kGeneral>
+// How scores are formed: scaled only; capped or with a bias by distance; the
+// same with a cap past pa::kCoarseCap (bf16).  A kernel each: a choice per call
+// inside took 2% of a decode step's time.
+enum { kPlain = 0, kGeneral = 1, kFineCap = 2 };
+
+template <typename T, int kForm>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 rows_kernel(const __grid_constant__ Args a, int items) {
   constexpr int D = kHeadDim, S = kStep<T>, NT = S / 8;  // tiles of 8 tokens in a step
@@ -249,7 +254,7 @@ rows_kernel(const __grid_constant__ Args a, int items) {
 #pragma unroll 1
   for (int s = 0; s < kStages - 1; ++s) load_next();
 
-  const float zs = kGeneral && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
+  const float zs = kForm != kPlain && a.softcap > 0.f ? a.scale / a.softcap : a.scale * pa::kLog2e;
   const float cap = a.softcap * pa::kLog2e;
   const bool whole_rows = a.prefix_parts + a.own_parts == 1;  // rows are finished here
 #pragma unroll 1
@@ -269,7 +274,7 @@ rows_kernel(const __grid_constant__ Args a, int items) {
       sp[h] = pa::Span{__shfl_sync(0xffffffffu, it.mine.lo, r), __shfl_sync(0xffffffffu, it.mine.hi, r),
                        __shfl_sync(0xffffffffu, it.mine.pos, r)};
       const int head = it.j * a.g + r % a.g;
-      slope[h] = kGeneral && a.slopes && r < it.nrows ? a.slopes[head] * pa::kLog2e : 0.f;
+      slope[h] = kForm != kPlain && a.slopes && r < it.nrows ? a.slopes[head] * pa::kLog2e : 0.f;
       row_at[h] = (it.row0 + r / a.g) * a.Hq + head;
       const T* q = static_cast<const T*>(a.q) + (it.row0 + r / a.g) * a.q_stride + (int64_t)head * D;
 #pragma unroll
@@ -322,8 +327,8 @@ rows_kernel(const __grid_constant__ Args a, int items) {
         for (int e = 0; e < 4; ++e) {
           const int h = e >> 1, u = u0 + n * 8 + (e & 1);
           float x = (z[n][e] + y[n][e]) * zs;
-          if (kGeneral) {
-            if (cap > 0.f) x = kBf16 ? pa::capped(x, cap) : cap * tanhf(x);
+          if (kForm != kPlain) {
+            if (cap > 0.f) x = !kBf16 ? cap * tanhf(x) : kForm == kFineCap ? pa::capped_fine(x, cap) : pa::capped(x, cap);
             x = fmaf(-slope[h], fabsf((float)(sp[h].pos - u)), x);
           }
           if (!whole && (u < sp[h].lo || u >= sp[h].hi || !(there >> (u & (S - 1)) & 1u))) x = -INFINITY;
@@ -554,7 +559,9 @@ int run(const PagedAttend& p, const Plan& pl, const Args& a, cudaStream_t st) {
   } else {
     const int64_t items = pl.prefix_items + pl.own_items * pl.own_parts;
     if (items > INT32_MAX / 2) return fail(HKV_ERR_UNSUPPORTED, "too many sequences and heads");
-    auto kernel = a.softcap > 0.f || a.slopes ? rows_kernel<T, true> : rows_kernel<T, false>;
+    auto kernel = a.softcap > 0.f || a.slopes ? rows_kernel<T, kGeneral> : rows_kernel<T, kPlain>;
+    if constexpr (sizeof(T) == 2)
+      if (a.softcap > pa::kCoarseCap) kernel = rows_kernel<T, kFineCap>;
     rc = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes),
                     "paged attention smem attribute");
     if (rc != HKV_OK) return rc;

@@ -175,16 +175,14 @@ __device__ __forceinline__ float2 exp2_poly(uint64_t x) {
   return make_float2(__int_as_float(__float_as_int(v.x) + (__float_as_int(n.x) << 23)),
                      __int_as_float(__float_as_int(v.y) + (__float_as_int(n.y) << 23)));
 }
-// cap * tanh(f v) for |f v| <= 1/2, as v * (c0 + c1 v^2 + c2 v^4 + c3 v^6): the odd
-// minimax polynomial of degree 7 (absolute error of the tanh 1.6e-7), with f
-// and cap multiplied into its coefficients once.
+// cap * tanh(f v) for |f v| <= 1/2, as v * (c0 + c1 v^2 + c2 v^4 + c3 v^6): the
+// polynomial of pa::capped, with f and cap multiplied into its coefficients once.
 struct CapPoly {
   float c[4];
   __device__ __forceinline__ CapPoly(float f, float cap) {
-    const float t[4] = {9.999976754e-01f, -3.332065642e-01f, 1.314514428e-01f, -4.337245598e-02f};
     float power = f * cap;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = t[i] * power, power *= f * f;
+    for (int i = 0; i < 4; ++i) c[i] = pa::kTanh[i] * power, power *= f * f;
   }
   __device__ __forceinline__ uint64_t factor(uint64_t v) const {
     const uint64_t u = mul2(v, v);
@@ -354,7 +352,9 @@ struct Loader {
 // a cap or a scale of any sign).
 enum { kPlain = 0, kCapped = 1, kBiased = 2 };
 
-template <bool kPrefix, int kMode>
+// kFineCap: the cap is past pa::kCoarseCap.  An instance each: a choice inside made
+// the code of the softmax longer (capped scores behind a prefix: 61 -> 65 us).
+template <bool kPrefix, int kMode, bool kFineCap>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ TcArgs t) {
@@ -646,7 +646,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           if (kMode != kPlain && cap > 0.f) {
             const float size = kMode == kBiased ? cap : 1.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(pa::capped(__uint_as_float(v[i]) * to_cap, size));
+            for (int i = 0; i < 32; ++i) {
+              const float x = __uint_as_float(v[i]) * to_cap;
+              v[i] = __float_as_uint(kFineCap ? pa::capped_fine(x, size) : pa::capped(x, size));
+            }
           }
           const float by = cap > 0.f ? 1.f : a.scale * pa::kLog2e;
 #pragma unroll
@@ -857,6 +860,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
   if constexpr (kPrefix) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const TcArgs);
+template <int kMode, bool kFineCap>
+Kernel pick(bool prefix) {
+  return prefix ? attend_tc_kernel<true, kMode, kFineCap> : attend_tc_kernel<false, kMode, kFineCap>;
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -936,9 +945,10 @@ int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int s
     t.box = box;
   }
   const int mode = a.slopes != nullptr || (!(a.scale > 0.f) && a.softcap == 0.f) ? kBiased : a.softcap > 0.f ? kCapped : kPlain;
-  auto kernel = mode == kBiased ? (prefix ? attend_tc_kernel<true, kBiased> : attend_tc_kernel<false, kBiased>)
-                : mode == kCapped ? (prefix ? attend_tc_kernel<true, kCapped> : attend_tc_kernel<false, kCapped>)
-                                  : (prefix ? attend_tc_kernel<true, kPlain> : attend_tc_kernel<false, kPlain>);
+  const bool fine = a.softcap > pa::kCoarseCap;
+  auto kernel = mode == kPlain ? pick<kPlain, false>(prefix)
+                : mode == kCapped ? (fine ? pick<kCapped, true>(prefix) : pick<kCapped, false>(prefix))
+                                  : (fine ? pick<kBiased, true>(prefix) : pick<kBiased, false>(prefix));
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return cuda_check(e, "attention smem attribute");
   const int64_t grid = (int64_t)t.tiles * splits * p.Hkv;

@@ -512,7 +512,7 @@ size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv
  *   cap(x) = softcap * tanh(x / softcap), or x when softcap is 0
  * and query row t sees the positions u with
  *   max(0, q_first[t], p + 1 - window) <= u < min(n, max(p + 1, prefix_len[b])).
- *   softcap     >= 0
+ *   softcap     0, or from |scale| / 2^16 to 2^100 (HKV_ERR_UNSUPPORTED otherwise)
  *   window      >= 0; 0: no window
  *   slopes      nullable, device fp32 [Hq]
  *   prefix_len  nullable, device int32 [B]: the first prefix_len[b] positions

@@ -413,6 +413,36 @@ def test_pages_before_the_first_seen_position_may_hold_anything(mask, new, dt, P
     check(out.cpu(), lse.cpu(), want, dt, score_error(q, toks[0], 1 / math.sqrt(D)), n)
 
 
+@pytest.mark.parametrize("cap", [3.0, 200.0, 1e4, 1e6, 1e9, 2.0 ** 100])
+@pytest.mark.parametrize("new, n, kw", [
+    (1, 700, {}), (3, 3000, dict(slopes=True)),                     # rows of 16, bf16
+    (300, 700, dict(window=200)), (60, 3000, {}),                   # row tiles: masked ones and whole ones in a row
+    (200, 500, dict(slopes=True)), (150, 400, dict(scale=-0.06)),
+    (9, 600, dict(dt=F32)),
+])
+def test_a_cap_of_any_size(new, n, kw, cap):
+    """Scores far below the cap are what they are without one.  The cap's own error is at most 2.6e-6 of the score: the
+    tanh of an argument below 1/2 by a polynomial whose linear coefficient lacks 2.4e-6, that of a larger one by an
+    exponential and a division of 2^-22 each, which count for at most 2^-20 of a score of 0.46 caps and more."""
+    kw = dict(kw)
+    dt, slopes, scale = kw.pop("dt", BF), kw.pop("slopes", False), kw.pop("scale", 1 / math.sqrt(D))
+    Hq, g = 4, torch.Generator().manual_seed(11)
+    toks, pool, table = _cache(1, n, dt=dt)
+    pool = pool.nan_to_num(0.0)
+    q = (4 * torch.randn(new, Hq, D, generator=g)).to(dt)
+    sl = 2.0 ** -torch.arange(3, 3 + Hq).float() if slopes else None
+    out, lse, st = torch.zeros(new, Hq, D, dtype=dt, device=DEV), torch.zeros(new, Hq, device=DEV), hkv.status_word()
+    hkv.hkv_prefill_attend_paged(q.to(DEV), pool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, scale=scale,
+                                 softcap=cap, slopes=None if sl is None else sl.to(DEV), status=st,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, dt), **kw)
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    pos, lo, hi = spans(n, new, kw.get("window", 0))
+    want = attend(q, toks[0], toks[0], pos, lo, hi, scale, cap, sl)
+    size = abs(scale) * float(q.double().norm(dim=-1).max() * toks[0].double().norm(dim=-1).max())
+    dz = score_error(q, toks[0], scale) + 2.6e-6 * min(cap, size) + (2.0 ** -23 * 0.125 * n if slopes else 0.0)
+    check(out.cpu(), lse.cpu(), want, dt, dz, n)
+
+
 def test_sequences_may_share_pages_and_calls_may_overlap():
     """The same pages in two sequences' tables, and two calls on two streams with a workspace each."""
     n, Hq, new = 900, 8, 40

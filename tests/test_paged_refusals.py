@@ -118,6 +118,20 @@ def test_prefill_refusals(lib, change, code, word):
         assert word in hkv.hkv_last_error()
 
 
+@pytest.mark.parametrize("scale, softcap, ok", [
+    (0.1, 0.0, True), (0.1, 30.0, True), (-0.1, 30.0, True), (0.1, 2.0 ** 100, True), (0.1, 2.0 ** -19, True),
+    (0.0, 1e-30, True), (0.1, 2.0 ** 101, False), (0.1, 1e-6, False), (-0.1, 1e-6, False), (0.1, 1e-45, False),
+])
+def test_caps_that_fp32_cannot_form(lib, scale, softcap, ok):
+    """A cap past 2^100, or below 2^-16 of the scale, is refused; one within goes on to the next check."""
+    a = {**PREFILL, "scale": scale, "cu": None, "score": ctypes.byref(_score(softcap=softcap))}
+    code = lib.hkv_prefill_attend_paged(*a.values())
+    assert code == (BAD if ok else UNS) and ("cu_q" if ok else "softcap") in hkv.hkv_last_error()
+    b = {**SHARED, "scale": scale, "score": ctypes.byref(_score(softcap=softcap))}
+    code = lib.hkv_shared_attend_paged(*b.values())
+    assert code == (CAP if ok else UNS) and ("needed" if ok else "softcap") in hkv.hkv_last_error()
+
+
 SHARED = dict(B=2, Hq=4, Hkv=2, dtype=BF, q=16, q_stride=512, K=16, V=16, ptable=16, prefix_pages=4, n_prefix=64, table=16,
               max_pages=2, num_pages=8, page=16, n=16, own_max=32, scale=0.1, score=None, out=16, lse=None, ws=None, ws_bytes=0,
               status=None, stream=None)
