@@ -477,8 +477,12 @@ typedef struct {
  * turned as well.  New token t (cu_new[b] <= t < cu_new[b + 1]) of sequence b
  * goes to position n_past[b] + t - cu_new[b] of its page table.
  *   hash       nullable: no codes are written.  hash->dtype must equal dtype.
- *              codes_pool (and norms_pool, SIGN only, nullable) get exactly
- *              what hkv_encode_keys gives for the stored keys
+ *              codes_pool (and norms_pool, SIGN only, nullable) get the codes
+ *              of the stored keys: exactly what hkv_encode_keys gives for SIGN;
+ *              for MLP and fp32 LSH what it gives for the call's T * Hkv stored
+ *              keys as its rows; for bf16 LSH, whose sums run in another order,
+ *              the same bits but where a projection is within 2^-16 of the sum
+ *              of its terms' magnitudes of zero
  *   rope       nullable: nothing is turned
  *   T          rows of q, k_new and v_new; rows from cu_new[B] on are ignored
  *   q, q_out   nullable together: [T, Hq, 128] in dtype; q_out may be q (same

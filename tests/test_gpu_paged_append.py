@@ -243,3 +243,53 @@ def test_two_calls_at_once():
     V = a["V_pool"].cpu()
     assert torch.equal(torch.cat([V[0, 0, 1:], V[1, 0, :1]]), a["v_new"][:, 0].cpu())
     assert torch.equal(V[4, 0], b["v_new"][:, 0].cpu())
+
+
+def _append_all(h, dt, T, Hkv, g, P=16):
+    """T tokens in one sequence, turned; returns the stored keys [T, Hkv, 128] and their codes."""
+    n = -(-T // P)
+    K, V = (torch.zeros(n, Hkv, P, D, dtype=dt, device=DEV) for _ in range(2))
+    codes = torch.zeros(n, Hkv, P, h.words, dtype=torch.int32, device=DEV)
+    k = torch.randn(T, Hkv, D, generator=g).to(dt).to(DEV)
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    st = hkv.status_word()
+    hkv.hkv_append_paged(h, k, k, K, V, torch.arange(n, dtype=torch.int32, device=DEV)[None], i([0, T]), i([0]), codes,
+                         rope=hkv.RopeParams(_inv(64).to(DEV)), ws=hkv.append_workspace(h, T, Hkv), status=st)
+    assert hkv.hkv_check(st) == hkv.HKV_OK
+    flat = lambda x: x.transpose(1, 2).reshape(n * P, Hkv, -1)[:T].contiguous()  # noqa: E731
+    return flat(K), flat(codes)
+
+
+@pytest.mark.parametrize("T, Hkv", [(1, 1), (37, 3), (900, 8)])
+@pytest.mark.parametrize("bits", [64, 128])
+def test_projected_bits_are_the_signs(bits, T, Hkv):
+    """bf16 LSH, bit by bit and no key left out: products of bf16 are exact in fp32, and 128 of them summed in any order,
+    each sum rounded or cut off, are off by at most 128 x 2^-23 = 2^-16 of their magnitudes' sum."""
+    g = torch.Generator().manual_seed(bits + T)
+    h = hkv.HashParams.lsh(torch.randn(bits, D, generator=g).bfloat16().to(DEV))
+    keys, codes = _append_all(h, torch.bfloat16, T, Hkv, g)
+    ref = torch.zeros(T * Hkv, h.words, dtype=torch.int32, device=DEV)
+    hkv.hkv_encode_keys(h, keys.view(-1, D), ref)
+    R, x = h.tensors[0].cpu().double(), keys.cpu().double().view(-1, D)
+    y, margin = x @ R.T, 2.0 ** -16 * (x.abs() @ R.abs().T)
+    sure = y.abs() > margin
+    assert sure.float().mean() > 0.999
+    shift = torch.arange(32)
+    for got in (codes.view(-1, h.words), ref):
+        b = (got.cpu()[:, :, None] >> shift & 1).reshape(len(x), bits).bool()
+        assert torch.equal(b[sure], (y > 0)[sure])
+
+
+@pytest.mark.parametrize("T, Hkv", [(1, 1), (37, 3), (300, 8), (2500, 4)])
+@pytest.mark.parametrize("kind, dt", [("mlp", torch.bfloat16), ("unpacked", torch.bfloat16), ("mlp", torch.float32),
+                                      ("lsh64", torch.float32), ("lsh128", torch.float32)])
+def test_staged_codes_are_the_encoders(kind, dt, T, Hkv):
+    """The hashes that go by way of the workspace: the codes that one call of the encoder gives for these keys."""
+    g = torch.Generator().manual_seed(T + Hkv)
+    h = _hash("mlp" if kind == "unpacked" else kind, dt, g)
+    if kind == "unpacked":
+        h.c.packed = None
+    keys, codes = _append_all(h, dt, T, Hkv, g)
+    ref = torch.zeros(T * Hkv, h.words, dtype=torch.int32, device=DEV)
+    hkv.hkv_encode_keys(h, keys.view(-1, D), ref)
+    assert torch.equal(codes.view(-1, h.words), ref)
