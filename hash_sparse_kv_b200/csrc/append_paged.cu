@@ -59,6 +59,7 @@ struct AppendArgs {
   const void* R;
   void* staged;  // kHashStage: the stored keys again, [T, Hkv, 128]
   PageMap pm;
+  uint64_t most;  // positions that have a place: those of the page table, as far as int32 goes
   int32_t* status;
   uint8_t axis[64];
 };
@@ -229,7 +230,7 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, int64_t t) {
   const int64_t first = a.cu[b], end = a.cu[b + 1];
   if (t < first || t >= end) return Place{-1, 0};
   const int64_t pos = (int64_t)a.n_past[b] + t - first;
-  if (pos < 0 || pos >= a.pm.max_pages * a.pm.page_size) return Place{-2, (int32_t)pos};
+  if ((uint64_t)pos >= a.most) return Place{-2, (int32_t)pos};
   const uint32_t P = a.pm.page_size, at = (uint32_t)pos / P;
   const int64_t page = a.pm.table[(int64_t)b * a.pm.max_pages + at];
   if (page < 0 || page >= a.pm.num_pages) return Place{-2, (int32_t)pos};
@@ -464,7 +465,7 @@ scatter_codes_kernel(const __grid_constant__ AppendArgs a, const uint32_t* __res
       const int b = pa::find_seq(a.cu, a.B, t);
       if (i >= n || i / a.Hkv != t) continue;
       const int64_t first = a.cu[b], end = a.cu[b + 1], pos = (int64_t)a.n_past[b] + t - first;
-      if (t < first || t >= end || pos < 0 || pos >= a.pm.max_pages * a.pm.page_size) continue;
+      if (t < first || t >= end || (uint64_t)pos >= a.most) continue;
       const int64_t page = a.pm.table[(int64_t)b * a.pm.max_pages + pos / a.pm.page_size];
       if (page < 0 || page >= a.pm.num_pages) continue;
       const int64_t row = (page * a.Hkv + i % a.Hkv) * a.pm.page_size + pos % a.pm.page_size;
@@ -508,6 +509,7 @@ int launch_append_paged(const AppendPaged& p, const PageMap& pm, void* ws, cudaS
   a.cu = p.cu_new, a.n_past = p.n_past, a.positions = p.positions;
   a.K = p.K_pool, a.V = p.V_pool, a.codes = p.codes_pool, a.norms = p.norms_pool;
   a.pm = pm, a.status = p.status;
+  a.most = pm.max_pages <= INT32_MAX / pm.page_size ? pm.max_pages * pm.page_size : 1ull << 31;
   if (p.rope) {
     a.pairs = p.rope->pairs, a.interleaved = p.rope->interleaved, a.inv_freq = p.rope->inv_freq;
     for (int i = 0; i < 64; ++i) a.axis[i] = p.rope->axis[i];

@@ -496,8 +496,8 @@ typedef struct {
  *              as above
  *   ws         hkv_append_paged_workspace_bytes bytes (0 for the bf16 LSH and
  *              the SIGN hash and without one); no zero fill needed
- * A position outside the page table or a page id outside the pool is reported
- * as HKV_ERR_DEVICE_RANGE and the token is not stored.  Two tokens with the
+ * A position outside the page table or past 2^31 - 1, or a page id outside the
+ * pool, is reported as HKV_ERR_DEVICE_RANGE and the token is not stored.  Two tokens with the
  * same place in the pool (a page that two sequences both extend) race.  One
  * launch for the hashes without a workspace, three otherwise. */
 int hkv_append_paged(const hkv_hash* hash, int dtype, const hkv_rope* rope, int B, int64_t T, int Hq, int Hkv,

@@ -293,3 +293,31 @@ def test_staged_codes_are_the_encoders(kind, dt, T, Hkv):
     ref = torch.zeros(T * Hkv, h.words, dtype=torch.int32, device=DEV)
     hkv.hkv_encode_keys(h, keys.view(-1, D), ref)
     assert torch.equal(codes.view(-1, h.words), ref)
+
+
+@pytest.mark.parametrize("kind", ["none", "mlp"])
+def test_the_last_positions_of_all(kind):
+    """A page table of more than 2^31 positions: the last one that int32 holds is stored and turned like any other, and
+    those behind it are reported and not stored."""
+    P, Hkv, T, g = 256, 2, 6, torch.Generator().manual_seed(2)
+    past, pages = (1 << 31) - 4, (1 << 31) // P + 1
+    h = _hash(kind, torch.bfloat16, g)
+    table = torch.full((1, pages), -1, dtype=torch.int32, device=DEV)
+    table[0, -2], table[0, -1] = 1, 0
+    K, V = (torch.zeros(2, Hkv, P, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    codes = None if h is None else torch.full((2, Hkv, P, h.words), -77, dtype=torch.int32, device=DEV)
+    x = torch.randn(T, Hkv, D, generator=g).bfloat16()
+    inv = (_inv(64) * 1e-3).float()  # angles that fp64 holds to the end
+    st = hkv.status_word()
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    hkv.hkv_append_paged(h, x.to(DEV), x.to(DEV), K, V, table, i([0, T]), i([past]), codes, rope=hkv.RopeParams(inv.to(DEV)),
+                         ws=hkv.append_workspace(h, T, Hkv), status=st)
+    assert hkv.hkv_check(st) == hkv.HKV_ERR_DEVICE_RANGE
+    want = turn(x, (past + torch.arange(T))[None], inv, [0] * 64, False)[:4]
+    got = K[1, :, P - 4:].cpu().transpose(0, 1)
+    size = x.double()[:4].abs().amax(-1, keepdim=True) * 2
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + 6 * 2.0 ** -24 * size).all()
+    assert torch.equal(V[1, :, P - 4:].cpu().transpose(0, 1), x[:4])
+    assert (K[1, :, :P - 4] == 0).all() and (K[0] == 0).all() and (V[0] == 0).all()
+    if h is not None:
+        assert (codes[0] == -77).all() and (codes[1, :, :P - 4] == -77).all()
