@@ -728,14 +728,14 @@ def _ck(dev: int, t: torch.Tensor, name: str, dtype, shape) -> None:
 
 def _ck_rows(dev: int, t: torch.Tensor, name: str, dtype, shape) -> int:
     """[T, heads, 128] with dense heads; the rows may be further apart (e.g. a slice of a fused projection).
-    Returns their distance."""
+    Returns their distance (of one row: the row itself)."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
         _need(t, name, dtype, shape=shape, contiguous=False)
         _here(t, name, dev)
     rows, heads, one = t.stride()
     if t.numel() and (one != 1 or (shape[1] > 1 and heads != 128)):
         raise ValueError(f"{name} must have dense heads")
-    return rows if shape[0] > 1 else max(rows, shape[1] * 128)
+    return rows if shape[0] > 1 else shape[1] * 128
 
 
 def _ck_ws(dev: int, ws: Optional[torch.Tensor], status: Optional[torch.Tensor]):

@@ -184,3 +184,12 @@ def test_binding_refusals(lib):
         hkv.RopeParams(torch.zeros(64))
     with pytest.raises(TypeError):
         hkv.prefill_workspace(1, 4, 2, 4, 4, 48, torch.float16)
+
+
+@pytest.mark.parametrize("stride", [1, 300, 6144 + 3])
+def test_one_row_has_no_distance(lib, stride):
+    """A single token's rows may be any distance apart, since there is no second one: it is not refused for it."""
+    one = torch.empty(1 << 14).as_strided((1, 2, 128), (stride, 128, 1))
+    assert hkv._ck_rows(-1, one, "q", torch.float32, (1, 2, 128)) == 256
+    two = torch.empty(1 << 14).as_strided((2, 2, 128), (6147, 128, 1))
+    assert hkv._ck_rows(-1, two, "q", torch.float32, (2, 2, 128)) == 6147  # for the library to judge
