@@ -241,7 +241,7 @@ class HashParams:
 
 def status_word(device=None) -> torch.Tensor:
     """A zeroed int32 device status word."""
-    return torch.zeros(1, dtype=torch.int32, device=device or "cuda")
+    return torch.zeros(1, dtype=torch.int32, device="cuda" if device is None else device)
 
 
 def hkv_version() -> str:
@@ -274,7 +274,7 @@ def workspace(B, Hq, Hkv, n_tokens, code_bits, top_k, n_sink=0, n_local=0, devic
     n = hkv_workspace_bytes(B, Hq, Hkv, n_tokens, code_bits, top_k, n_sink, n_local)
     if n == 0 and B * Hkv * max(top_k, 1) > 0:
         raise HkvError(HKV_ERR_UNSUPPORTED, hkv_last_error() or "unsupported shape")
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def hkv_encode_keys(h: HashParams, x: torch.Tensor, codes: torch.Tensor, norms: Optional[torch.Tensor] = None,
@@ -458,7 +458,7 @@ def normw_workspace(B, Hkv, n_tokens, n_sink, n_local, top_k, device=None) -> Op
     """The workspace of hkv_retrieve_topk_normw for this shape, or None when
     the call runs one block per KV head without one."""
     n = hkv_normw_workspace_bytes(B, Hkv, n_tokens, n_sink, n_local, top_k)
-    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def hkv_retrieve_topk_normw(q_codes, k_codes, norms, n_tokens: int, n_sink: int, n_local: int, top_k: int, idx,
@@ -651,7 +651,7 @@ def normw_decode_workspace(B, Hq, Hkv, n_tokens, code_bits, top_k, n_sink=0, n_l
     n = hkv_workspace_bytes(B, Hq, Hkv, n_tokens, code_bits, top_k, n_sink, n_local)
     if n == 0 and B * Hkv * max(top_k, 1) > 0:
         raise HkvError(HKV_ERR_UNSUPPORTED, hkv_last_error() or "unsupported shape")
-    return torch.zeros(a + max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(a + max(n, 256), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def hkv_decode_step_normw(q, k_codes, norms, K, V, n_tokens: int, n_sink: int, n_local: int, top_k: int, idx, out,
@@ -843,7 +843,7 @@ def hkv_prefill_workspace_bytes(B, Hq, Hkv, T, max_q, n_tokens_max, dtype: int) 
 
 
 def _scratch(n: int, device) -> Optional[torch.Tensor]:
-    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def prefill_workspace(B, Hq, Hkv, T, max_q, n_tokens_max, dtype=torch.bfloat16, device=None) -> Optional[torch.Tensor]:

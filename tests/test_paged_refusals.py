@@ -193,3 +193,18 @@ def test_one_row_has_no_distance(lib, stride):
     assert hkv._ck_rows(-1, one, "q", torch.float32, (1, 2, 128)) == 256
     two = torch.empty(1 << 14).as_strided((2, 2, 128), (6147, 128, 1))
     assert hkv._ck_rows(-1, two, "q", torch.float32, (2, 2, 128)) == 6147  # for the library to judge
+
+
+def test_a_workspace_is_on_the_device_that_is_named(lib, monkeypatch):
+    """Device 0 too, when it is not the current one; without a name the current one."""
+    seen = []
+    monkeypatch.setattr(hkv, "hkv_workspace_bytes", lambda *a: 64)  # without a device there is no plan
+    for name in ("empty", "zeros"):
+        monkeypatch.setattr(torch, name, lambda *a, **k: seen.append(k.get("device")))
+    for device, want in ((0, 0), (1, 1), ("cuda:0", "cuda:0"), (None, "cuda")):
+        seen.clear()
+        hkv.status_word(device)
+        hkv.workspace(1, 4, 2, 100, 128, 8, device=device)
+        hkv.normw_decode_workspace(1, 4, 2, 100, 128, 8, device=device)
+        hkv.shared_workspace(2, 4, 2, 64, 32, device=device)
+        assert [d for d in seen if d is not None] == [want] * 4
