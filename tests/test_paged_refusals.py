@@ -200,7 +200,10 @@ def test_a_workspace_is_on_the_device_that_is_named(lib, monkeypatch):
     seen = []
     monkeypatch.setattr(hkv, "hkv_workspace_bytes", lambda *a: 64)  # without a device there is no plan
     for name in ("empty", "zeros"):
-        monkeypatch.setattr(torch, name, lambda *a, **k: seen.append(k.get("device")))
+        def made(*a, real=getattr(torch, name), device=None, **k):
+            seen.append(device)
+            return real(0, **k)
+        monkeypatch.setattr(torch, name, made)
     for device, want in ((0, 0), (1, 1), ("cuda:0", "cuda:0"), (None, "cuda")):
         seen.clear()
         hkv.status_word(device)
