@@ -69,6 +69,7 @@ struct TcArgs {
   int tiles;     // row tiles of 256 (at most), all sequences together
   int splits;
   int part0;     // first partial of this launch; -1: rows are finished here
+  int drop;      // testing aid: tiles of keys at the end that are never loaded
 };
 
 // ---- instructions beside those of tc.cuh -----------------------------------
@@ -482,7 +483,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (t.box == 0 && t0 < t1) ld.look(t0);
       int stage = 0, armed = 0;
       uint32_t phase = 0;
-      for (int n = t0; n < t1; ++n) {
+      for (int n = t0; n < t1 - (is_k ? t.drop : 0); ++n) {
         if (!all(tc::mbar_try_wait(&empty[stage], phase ^ 1u))) {
           ld.settle<0>();  // what waits for the tile before may be what this one waits for
           if (!all(wait(&empty[stage], phase ^ 1u, abort, a.wait_ns))) break;
@@ -778,6 +779,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       if (lane == 0) tc::mbar_arrive(&p_full[slot]);
       ++done, ++at_turn;
     }
+    tmem_wait_st();  // a loop left on an abort may have stores on their way
     if (done > 0) {
       const bool ok = wait(&o_done[slot], (done - 1) & 1, abort, a.wait_ns);
       __all_sync(0xffffffffu, ok);
@@ -803,7 +805,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       }
       softmax_barrier();
     }
-    if (active && (both || slot == 0) && !*abort) {
+    if (active && (both || slot == 0) && all(*abort == 0)) {
       float scale0 = 1.f;
       if (!both) {
         const float m1 = other[kTile * kTile + row], l1 = other[kTile * kTile + kTile + row];
@@ -931,7 +933,7 @@ int tc_splits(const PagedAttend& p, bool prefix, int sms) {
 }
 
 int launch_attend_tc(const PagedAttend& p, const pa::Args& a, bool prefix, int splits, int part0, cudaStream_t st) {
-  TcArgs t{a, 0, (int)tc_tiles(p, prefix), splits, part0};
+  TcArgs t{a, 0, (int)tc_tiles(p, prefix), splits, part0, debug_flags() & kDebugDropTile ? 1 : 0};
   // the largest power of two that divides the page: a box never leaves its
   // page, and whole swizzle groups of 8 rows keep the tile's layout
   int box = p.pm.page_size & -p.pm.page_size;

@@ -20,7 +20,7 @@ uint64_t wait_limit_ns();
 int sm_count();
 int max_smem_optin();  // opt-in dynamic shared memory per block, bytes
 
-constexpr int kDebugSkipArrive = 1;
+constexpr int kDebugSkipArrive = 1, kDebugDropTile = 2;
 
 // ---- encoders (encode.cu) ----
 int launch_encode(const hkv_hash& h, const void* x, const RowMap& m, uint32_t* codes,

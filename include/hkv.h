@@ -628,8 +628,10 @@ int hkv_decode_step(const hkv_hash* q_hash, int B, int Hq, int Hkv, const void* 
 
 /* Testing aid (process-wide).  flags bit 0: in the next retrieval launches,
  * block 0 does not signal its arrival at the cross-block wait, so the wait
- * runs out and reports HKV_ERR_TIMEOUT.  wait_limit_ns: limit of every
- * cross-block wait (0 restores the default of 2 s). */
+ * runs out and reports HKV_ERR_TIMEOUT.  Bit 1: in the next launches of the
+ * prompts' and shared prefixes' tile kernel no CTA loads its last tile of keys,
+ * so the waits for it run out, with the same report.  wait_limit_ns: limit of
+ * every such wait (0 restores the default of 2 s). */
 int hkv_debug_set(int flags, int64_t wait_limit_ns);
 
 #ifdef __cplusplus
