@@ -443,6 +443,30 @@ def test_a_cap_of_any_size(new, n, kw, cap):
     check(out.cpu(), lse.cpu(), want, dt, dz, n)
 
 
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("new, n", [(1, 900), (40, 300)])
+def test_fp32_keys_that_are_no_numbers(new, n, value):
+    """A seen infinity counts as a NaN in fp32; behind a window, neither counts for anything."""
+    Hq, at, window = 4, n - new // 2 - 30, 64
+    toks, pool, table = _cache(1, n, dt=F32)
+    kpool = pool.clone()
+    kpool[int(table[0, at // 16]), 1, at % 16, 5] = value
+    kpool[int(table[0, 0]), :, 3] = value  # before every window
+    q = torch.randn(new, Hq, D, generator=torch.Generator().manual_seed(6))
+    out, lse = torch.zeros(new, Hq, D, device=DEV), torch.zeros(new, Hq, device=DEV)
+    hkv.hkv_prefill_attend_paged(q.to(DEV), kpool, pool, table, _i([0, new]), _i([n]), new, n, out, lse=lse, window=window,
+                                 ws=hkv.prefill_workspace(1, Hq, 2, new, new, n, F32))
+    pos, lo, hi = spans(n, new, window)
+    hit = torch.zeros(new, Hq, dtype=torch.bool)
+    hit[(lo <= at) & (at < hi), 2:] = True
+    assert hit.any()
+    assert torch.equal(out.cpu().isnan().all(-1), hit) and torch.equal(out.cpu().isnan().any(-1), hit)
+    assert torch.equal(lse.cpu().isnan(), hit)
+    want = attend(q, toks[0], toks[0], pos, lo, hi, 1 / math.sqrt(D))
+    check(torch.where(hit[..., None], want[0].float(), out.cpu()), torch.where(hit, want[1].float(), lse.cpu()), want, F32,
+          score_error(q, toks[0], 1 / math.sqrt(D)), n)
+
+
 def test_sequences_may_share_pages_and_calls_may_overlap():
     """The same pages in two sequences' tables, and two calls on two streams with a workspace each."""
     n, Hq, new = 900, 8, 40
