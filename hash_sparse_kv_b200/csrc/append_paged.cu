@@ -21,11 +21,14 @@
 // memory (mma.sync m16n8k16: the 2 * 128 * bits flops per key are far below
 // what the key's own traffic allows).
 //
-// Bound by memory, with the arithmetic of the turn close behind (16384 prompt
-// tokens of 32 / 8 heads with sign codes: 70 us, 5.4 TB/s, the ALU busy 55% of
-// the time); with the projection (8192 tokens, 64 bits: 61 us, 3.9 TB/s) by the
-// loads that 24 warps an SM can keep on their way.  One token takes 5 us, a
-// chain of latencies: the sequence and its page, the angles, the rows.
+// Bound by memory, with the arithmetic of the turn close behind (15396 prompt
+// tokens of 32 / 8 heads with sign codes: 71 us, 5.4 TB/s, the ALU busy 55% of
+// the time); with the projection (9725 tokens, 64 bits: 61.5 us, 3.9 TB/s, 49
+// without a hash) by the loads that 24 warps an SM can keep on their way, none
+// of them while a step is hashed.  One token takes 5 us, a chain of latencies:
+// the sequence and its page, the angles, the rows.  (Device times of a captured
+// graph; among other calls 75, 63.5 and 14.)  Hashes by way of the workspace, for
+// the same 9725 tokens: MLP of 128 units and bits 74 us, fp32 LSH 177.
 #include <cstdio>
 
 #include "attend_paged.cuh"
@@ -38,10 +41,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRowLanes = 8;                     // lanes of one row
 constexpr int kKeyPitch = kHeadDim + 8;          // shared key rows: 272 bytes, conflict-free for ldmatrix
 constexpr int kMaxKeys = 64;                     // keys of a step in shared memory, unless one token has more
-// Blocks per SM.  More warps hide the memory's latency best (16K prompt tokens
-// with the sign hash: 84, 76 and 72 us with two, three and four); the
-// projection's blocks, 70 KB each, fit three times, so their warps have two
-// groups of rows on their way instead of one.
+// Blocks per SM.  More warps hide the memory's latency best (15396 prompt tokens
+// with the sign hash: 84, 76 and 72 us with two, three and four).  The
+// projection's blocks are three, since with 128 bits and 64 keys a step they take
+// 70 KB each, and 76 registers a thread: their warps have two groups of rows on
+// their way instead of one.
 enum { kHashNone = 0, kHashSign = 1, kHashLsh = 2, kHashStage = 3 };
 constexpr int blocks_per_sm(int hash) { return hash == kHashLsh ? 3 : 4; }
 

@@ -14,14 +14,15 @@
 // one is finished, so that the eight warps of an SM keep 128 KB on their way
 // without ever waiting for each other.  The work is bound by reading K and V: a
 // 128-row tcgen05 tile would be seven eighths padding, so scores and products
-// are mma.sync with the 16 rows as M.  64 sequences of up to 8192 tokens (bf16,
-// capped scores) take 269 to 285 us, 5.7 to 6.1 TB/s.  fp32 is bound by the
-// latency of its three dependent products instead: chunks of 37 tokens behind
-// 900 take 26 us.
+// are mma.sync with the 16 rows as M.  64 sequences of 4259 to 8172 tokens
+// (bf16, capped scores) take 284 to 288 us, 5.7 TB/s.  fp32 is bound by the
+// latency of its three dependent products instead: chunks of 47, 41 and 35
+// tokens behind 520 to 893 take 25 us, 16 single tokens over 4344 to 8088 tokens
+// 234 us, 3.5 TB/s.
 //   bf16: m16n8k16; P is rounded to bf16 for the product, sums stay fp32.
 //   fp32: m16n8k8 tf32 in three products.  x = hi + lo, both of tf32's 11 bits;
-//         hi hi + hi lo + lo hi leaves out lo lo and the rounding of lo, each
-//         2^-22 of a product at most and without a sign of its own.
+//         hi hi + hi lo + lo hi leaves out lo lo (2^-22 of a product at most)
+//         and the rounding of both lo (2^-21.5 each), without a sign of their own.
 #include <cstdio>
 
 #include "attend_paged.cuh"

@@ -18,8 +18,10 @@
 // What bounds it: the products, 2 x 128 x 128 x 256 flops a tile and slot, and
 // beside them as much time of exponentials, which is why a slot weighs scores
 // while the other multiplies.  A causal prompt of 8192 tokens (32 query heads, 8
-// KV heads) takes 465 us, 1.18 PFLOP/s or 71% of a large library product's rate;
-// 256 sequences behind 98304 tokens 376 us, 1.10 PFLOP/s.  With 256 rows of one
+// KV heads) takes 471 us in a burst, 1.17 PFLOP/s or 70% of a large library
+// product's rate, and 550 us in a long run under the power cap (1.00); 256
+// sequences behind 98304 tokens 382 us (1.08) and 447; the same prompt in eight
+// documents 121 us (0.57), whose rows see 1024 tokens at most.  With 256 rows of one
 // KV head the tiles' reads (2 x 32 KB for 16.8 MFLOP) stay far below the
 // memory's rate.  Where the rows are few or see little (chunks in a window,
 // short documents) a CTA's start and end, 7.5 us, and its longest row tile show.

@@ -523,7 +523,9 @@ size_t hkv_append_paged_workspace_bytes(const hkv_hash* hash, int64_t T, int Hkv
  *               are seen by every query of the sequence (as far as the window
  *               and q_first let them), also by the earlier ones
  *   q_first     nullable, device int32 [T]: the first position that a query
- *               sees, e.g. the start of its document
+ *               sees, e.g. the start of its document.  There is no last one:
+ *               with prefix_len a query sees the prefix as far as it lies
+ *               behind its first position, later documents in it included
  * Keys that a query does not see may hold anything; a NaN in one that it sees,
  * or in the query, whatever its bits, makes its out and lse NaN, and so does an
  * infinity in fp32.  Values must be finite (fp32: below 2^128 - 2^116)
@@ -554,7 +556,11 @@ typedef struct {
  *            they plan the launch and size the workspace.  A sequence past
  *            them is cut to them and reported as HKV_ERR_DEVICE_RANGE
  *   score    nullable: plain causal attention
- *   out      [T, Hq, 128] in dtype;  lse nullable [T, Hq] fp32
+ *            (with B, T or max_q 0 nothing runs, and nothing is reported)
+ *   out      [T, Hq, 128] in dtype;  lse nullable [T, Hq] fp32.  Sums and
+ *            softmax statistics are fp32; in bf16 a weight is rounded to bf16
+ *            for its product with the value, in fp32 products are three of tf32
+ *            parts (off by at most 2^-20 of their size)
  *   ws       hkv_prefill_workspace_bytes bytes (may be 0), 256-byte aligned; no
  *            zero fill, and nothing in it outlives the call.  Calls that
  *            share one must not overlap on the GPU
