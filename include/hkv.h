@@ -554,9 +554,11 @@ typedef struct {
  *   cu_q     device int32 [B + 1], ascending from 0;  n_tokens_b device int32 [B]
  *   max_q, n_tokens_max   upper bounds of a sequence's new tokens and tokens;
  *            they plan the launch and size the workspace.  A sequence past
- *            them is cut to them and reported as HKV_ERR_DEVICE_RANGE
+ *            them counts as one of that length (its first max_q rows, the
+ *            last of n_tokens_max tokens) and is reported as
+ *            HKV_ERR_DEVICE_RANGE; with B, T or max_q 0 nothing runs, and
+ *            nothing is reported
  *   score    nullable: plain causal attention
- *            (with B, T or max_q 0 nothing runs, and nothing is reported)
  *   out      [T, Hq, 128] in dtype;  lse nullable [T, Hq] fp32.  Sums and
  *            softmax statistics are fp32; in bf16 a weight is rounded to bf16
  *            for its product with the value, in fp32 products are three of tf32
